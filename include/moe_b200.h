@@ -76,6 +76,11 @@ typedef enum {
                                   e4m3 activations (FP8 x FP4)                */
 } moe_wtype_t;
 
+typedef enum {
+    MOE_OUT_BF16 = 0,          /* rounded once from the fp32 accumulator     */
+    MOE_OUT_FP32 = 1
+} moe_otype_t;
+
 /* Version of this ABI (incremented on any incompatible change). */
 MOE_API int moe_abi_version(void);
 
@@ -417,6 +422,114 @@ MOE_API moe_status_t quantize_fp8_block128(const void *x, int rows, int cols, vo
 MOE_API moe_status_t moe_debug_permute(const int32_t *top_k_index, int T, int K, int E, int32_t *counts,
                                int32_t *offsets, int32_t *perm, int32_t *inv, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/*
+ * ---------------------------------------------------------------- training --
+ * The operators of the expert layer's training step.  The pages describe the
+ * forward only; these add its gradients around the same data: rows in expert
+ * order (moe_debug_permute gives offsets and inv), the expert weights in the
+ * layouts of moe_experts_prefill, the E4M3 rule of quantize_fp8_block128.
+ * All are bf16 in, accumulate in fp32 and round once to the output type.
+ *
+ * Products grouped by expert.  Rows [offsets[e], offsets[e+1]) of the row
+ * matrices belong to expert e, w is [E,N,C]:
+ *   moe_grouped_mm        y  [rows,N]: y[r]  = w[e] x[r]
+ *   moe_grouped_mm_dgrad  dx [rows,C]: dx[r] = w[e]^T dy[r]
+ *   moe_grouped_mm_wgrad  dw [E,N,C]:  dw[e] = base[e] + sum over r of dy[r] x[r]^T
+ * (gate_up: N = 2F, C = H; down: N = H, C = F).
+ *
+ *   x        [rows,C] bf16, dy [rows,N] bf16, w [E,N,C] bf16
+ *   offsets  [E+1] int32 on the device, non-decreasing, within [0, rows]
+ *            (values outside are clamped: the kernel reads and writes nothing
+ *            outside the matrices, but decreasing offsets give some rows to
+ *            two experts and leave the results of those rows undefined).
+ *            Experts may be empty.  Rows before offsets[0] and from
+ *            offsets[E] on belong to no expert: their outputs stay as they
+ *            were and their values, whatever they hold, reach no sum.
+ *   rows >= 0 (the row matrices' height; 0: nothing to do, wgrad writes
+ *            zeros or the base), at most 2^27
+ *   N, C     multiples of 8, 8 .. 65536; 1 <= E <= 1024
+ *   out_type of y, dx, dw
+ *   base     [E,N,C] fp32 or NULL (zeros); fp32 dw only.  It may be dw itself
+ *            (accumulation in place) and must not overlap it otherwise
+ *   workspace  >= 8192 bytes, 256-byte aligned, its header zero before first
+ *            use; only its status word is used (moe_workspace_status), so
+ *            calls that overlap may share it
+ * x, dy, w, y, dx, dw, base 16-byte aligned; outputs must not overlap inputs
+ * (but for base).  Fixed summation order: equal inputs give equal bits.
+ */
+MOE_API moe_status_t moe_grouped_mm(const void *x, const int32_t *offsets, const void *w, int rows, int N,
+                                    int C, int E, moe_otype_t out_type, void *y, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+MOE_API moe_status_t moe_grouped_mm_dgrad(const void *dy, const int32_t *offsets, const void *w, int rows,
+                                          int N, int C, int E, moe_otype_t out_type, void *dx,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, const int32_t *offsets, int rows,
+                                          int N, int C, int E, moe_otype_t out_type, const float *base,
+                                          void *dw, void *workspace, size_t workspace_bytes,
+                                          void *stream);
+
+/*
+ * SwiGLU with an 8-bit activation checkpoint.  With g = gate_up[r,0:F],
+ * u = gate_up[r,F:2F], a = g * sigmoid(g), p = row_weights[r] (1 when NULL):
+ *   h[r] = bf16(p * a * u)
+ *   codes[r], scale[r] = the 2F values of the row by the rule of
+ *                        quantize_fp8_block128 (per 128 columns)
+ * computed in fp32 from the bf16 values.  A block with an infinity takes the
+ * scale of the largest finite value, 2^120: code * scale gives the infinities
+ * back as infinities (as it does, by the rule's rounding, for finite values
+ * from 1.9375 * 2^127 on) and NaN as NaN.
+ *
+ *   gate_up  [rows,2F] bf16;  h [rows,F] bf16;  codes [rows,2F] E4M3 bytes;
+ *   scale    [rows,2F/128] fp32;  row_weights [rows] fp32 or NULL
+ *   n_rows   device int32 or NULL: only rows [0, *n_rows) are processed
+ *            (clamped to [0, rows]), the others stay as they were
+ *            (&offsets[E] of the routing)
+ *   rows >= 0, at most 2^27; F % 128 == 0, F <= 16384
+ *
+ * moe_swiglu_checkpoint_backward recomputes from codes and scale (g, u =
+ * code * scale; dh = gradient of the down product's input, before p):
+ *   dgate_up[r,0:F]  = bf16(p * dh * u * (s + a * (1 - s))),  s = sigmoid(g)
+ *   dgate_up[r,F:2F] = bf16(p * dh * a)
+ *   h[r]             = bf16(p * a * u)       (NULL: not written)
+ *   drow_weights[r]  = sum over f of dh * a * u, fp32  (NULL: not written)
+ * gate_up, h, codes, dh, dgate_up 16-byte aligned; outputs must not overlap
+ * inputs.
+ */
+MOE_API moe_status_t moe_swiglu_checkpoint(const void *gate_up, const float *row_weights,
+                                           const int32_t *n_rows, int rows, int F, void *h, void *codes,
+                                           float *scale, void *stream);
+MOE_API moe_status_t moe_swiglu_checkpoint_backward(const void *codes, const float *scale, const void *dh,
+                                                    const float *row_weights, const int32_t *n_rows,
+                                                    int rows, int F, void *dgate_up, void *h,
+                                                    float *drow_weights, void *stream);
+
+/*
+ * Rows from token order to expert order and back; each is the gradient of
+ * the other.  inv [T,top_k] int32 is the position of every slot in expert
+ * order (moe_debug_permute's inv); positions outside [0, n_rows) are skipped
+ * (dropped slots hold -1).
+ *   moe_permute_rows    rows[inv[t,k]] = x[t]; row_weights[inv[t,k]] =
+ *       top_k_weights[t,k].  x [T,H] bf16, or with x_scale [T,H/128] fp32
+ *       (H % 128 == 0) E4M3 codes of quantize_fp8_block128, restored as
+ *       bf16(code * scale).  Positions must be distinct (two slots with one
+ *       position leave either slot's values there); rows that no slot names
+ *       stay as they were.  top_k_weights and row_weights: both or neither.
+ *   moe_unpermute_rows  out[t] = bf16(sum over k ascending of y[inv[t,k]] +
+ *       residual[t]), summed in fp32; dtop_k_weights[t,k] =
+ *       drow_weights[inv[t,k]], 0 for a skipped slot.  y [n_rows,H] of
+ *       y_type, residual [T,H] bf16 or NULL; drow_weights [n_rows] and
+ *       dtop_k_weights [T,top_k]: both or neither.
+ *   0 <= T <= 2^24, 1 <= top_k <= 16, H % 8 == 0, 8 <= H <= 65536,
+ *   0 <= n_rows <= 2^27.  x, rows, y, residual, out 16-byte aligned.
+ */
+MOE_API moe_status_t moe_permute_rows(const void *x, const float *x_scale, const int32_t *inv,
+                                      const float *top_k_weights, int top_k, int T, int H, int n_rows,
+                                      void *rows, float *row_weights, void *stream);
+MOE_API moe_status_t moe_unpermute_rows(const void *y, moe_otype_t y_type, const int32_t *inv,
+                                        const void *residual, const float *drow_weights, int top_k,
+                                        int T, int H, int n_rows, void *out, float *dtop_k_weights,
+                                        void *stream);
 
 #ifdef __cplusplus
 }

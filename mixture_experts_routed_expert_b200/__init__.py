@@ -34,7 +34,9 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_experts_workspace_size",
            "moe_experts_shared_workspace_size", "moe_experts_with_shared",
            "moe_experts_decode_fused", "moe_stage_inputs", "moe_workspace_init",
            "moe_workspace_status", "moe_debug_decode_withhold", "moe_experts_rows",
-           "moe_combine_rows")
+           "moe_combine_rows", "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad",
+           "moe_swiglu_checkpoint", "moe_swiglu_checkpoint_backward", "moe_permute_rows",
+           "moe_unpermute_rows")
 
 
 def _load():
@@ -65,11 +67,21 @@ def _load():
     L.moe_debug_decode_withhold.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P, Z, I, P]
     L.moe_experts_rows.argtypes = [P, P, P, P, P, I, I, I, I, I, I, P, P, P, Z, P, P]
     L.moe_combine_rows.argtypes = [P, P, I, I, I, I, P, P]
+    mm = [P, P, P, I, I, I, I, I, P, P, Z, P]
+    L.moe_grouped_mm.argtypes = mm
+    L.moe_grouped_mm_dgrad.argtypes = mm
+    L.moe_grouped_mm_wgrad.argtypes = [P, P, P, I, I, I, I, I, P, P, P, Z, P]
+    L.moe_swiglu_checkpoint.argtypes = [P, P, P, I, I, P, P, P, P]
+    L.moe_swiglu_checkpoint_backward.argtypes = [P, P, P, P, P, I, I, P, P, P, P]
+    L.moe_permute_rows.argtypes = [P, P, P, P, I, I, I, I, P, P, P]
+    L.moe_unpermute_rows.argtypes = [P, I, P, P, P, I, I, I, I, P, P, P]
     for n in ("moe_experts_prefill", "moe_experts_decode", "moe_route_sigmoid_grouped",
               "quantize_fp8_block128", "moe_debug_permute", "moe_experts_decode_static",
               "moe_experts_with_shared", "moe_experts_decode_fused", "moe_stage_inputs",
               "moe_workspace_init", "moe_workspace_status", "moe_debug_decode_withhold",
-              "moe_experts_rows", "moe_combine_rows"):
+              "moe_experts_rows", "moe_combine_rows", "moe_grouped_mm", "moe_grouped_mm_dgrad",
+              "moe_grouped_mm_wgrad", "moe_swiglu_checkpoint", "moe_swiglu_checkpoint_backward",
+              "moe_permute_rows", "moe_unpermute_rows"):
         getattr(L, n).restype = I
     return L
 
@@ -389,3 +401,285 @@ def moe_debug_permute(top_k_index, E, workspace=None, stream=None):
                                _ptr(inv), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "moe_debug_permute")
     return counts, offsets, perm[:T * K], inv[:T * K]
+
+
+# ---- the training step's operators -----------------------------------------
+# Tensors may live on any device: the call is made on the tensors' device, on
+# `stream` (default: that device's current stream).  With a stream given,
+# outputs are allocated on it and the inputs are recorded as in use by it.
+
+_OTYPE = {torch.bfloat16: 0, torch.float32: 1}   # moe_otype_t
+
+
+def _want(what, t, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
+
+
+def _codes(what, t, shape):
+    if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError("%s must be E4M3 codes (uint8 / float8_e4m3fn), got %s" % (what, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
+
+
+def _one_device(*tensors):
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.device != dev):
+            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+    return dev
+
+
+def _new(shape, dtype, dev, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _header_workspace(workspace, dev, stream):
+    """The caller's workspace (its size is checked by the library), or a fresh zeroed header."""
+    if workspace is not None:
+        return workspace
+    if stream is None:
+        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=dev)
+
+
+def _enqueue(name, dev, stream, tensors, *args):
+    """Call entry point `name` with args and the stream, on device `dev`."""
+    fn = getattr(_lib(), name)
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("%s: the stream belongs to %s, the tensors to %s" % (name, stream.device, dev))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream)
+    elif dev.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(rc, name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out_type(out, out_dtype):
+    dt = out_dtype if out is None else out.dtype
+    if dt not in _OTYPE or (out is not None and out_dtype is not None and out_dtype != dt):
+        raise TypeError("the output must be bf16 or fp32 (and out of out_dtype), got %s" % dt)
+    return dt
+
+
+def _grouped(name, a, offsets, w, transpose, out, out_dtype, workspace, stream):
+    if w.dim() != 3 or a.dim() != 2:
+        raise ValueError("%s takes rows [rows, features] and weights [E, N, C]" % name)
+    E, N, C = w.shape
+    rows = a.shape[0]
+    ci, co = (N, C) if transpose else (C, N)
+    _want("the row matrix", a, torch.bfloat16, (rows, ci))
+    _want("w", w, torch.bfloat16, (E, N, C))
+    _want("offsets", offsets, torch.int32, (E + 1,))
+    if out is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    dt = _out_type(out, out_dtype)
+    dev = _one_device(a, offsets, w, out, workspace)
+    if out is None:
+        out = _new((rows, co), dt, dev, stream)
+    else:
+        _want("out", out, dt, (rows, co))
+    workspace = _header_workspace(workspace, dev, stream)
+    _enqueue(name, dev, stream, (a, offsets, w, out, workspace), a.data_ptr(), offsets.data_ptr(), w.data_ptr(),
+             rows, N, C, E, _OTYPE[dt], out.data_ptr(), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
+    return out
+
+
+def moe_grouped_mm(x, offsets, w, out=None, out_dtype=None, workspace=None, stream=None):
+    """y [rows, N]: y[r] = w[e] x[r] for the rows [offsets[e], offsets[e+1]) of each expert e.
+    x [rows, C] bf16, offsets [E+1] int32, w [E, N, C] bf16 -> bf16 (or out_dtype fp32).
+    Rows of no expert are not written."""
+    return _grouped("moe_grouped_mm", x, offsets, w, False, out, out_dtype, workspace, stream)
+
+
+def moe_grouped_mm_dgrad(dy, offsets, w, out=None, out_dtype=None, workspace=None, stream=None):
+    """dx [rows, C]: dx[r] = w[e]^T dy[r], the gradient of moe_grouped_mm's x.
+    dy [rows, N] bf16, w [E, N, C] bf16 -> bf16 (or out_dtype fp32)."""
+    return _grouped("moe_grouped_mm_dgrad", dy, offsets, w, True, out, out_dtype, workspace, stream)
+
+
+def moe_grouped_mm_wgrad(dy, x, offsets, base=None, out=None, out_dtype=None, workspace=None, stream=None):
+    """dw [E, N, C]: dw[e] = base[e] + sum over e's rows of dy[r] x[r]^T, the gradient of moe_grouped_mm's w.
+    dy [rows, N] bf16, x [rows, C] bf16 -> bf16 (or fp32).  base [E, N, C] fp32 (fp32 output) may be
+    `out` itself: the gradient is then accumulated in place.  Experts without rows get zeros (or base)."""
+    if dy.dim() != 2 or x.dim() != 2 or offsets.dim() != 1:
+        raise ValueError("moe_grouped_mm_wgrad takes rows [rows, N] and [rows, C] and offsets [E+1]")
+    rows, N = dy.shape
+    C, E = x.shape[1], offsets.shape[0] - 1
+    _want("dy", dy, torch.bfloat16, (rows, N))
+    _want("x", x, torch.bfloat16, (rows, C))
+    _want("offsets", offsets, torch.int32, (E + 1,))
+    if out is None and out_dtype is None:
+        out_dtype = torch.bfloat16 if base is None else torch.float32
+    dt = _out_type(out, out_dtype)
+    if base is not None:
+        if dt != torch.float32:
+            raise TypeError("base needs an fp32 output")
+        _want("base", base, torch.float32, (E, N, C))
+    dev = _one_device(dy, x, offsets, base, out, workspace)
+    if out is None:
+        out = _new((E, N, C), dt, dev, stream)
+    else:
+        _want("out", out, dt, (E, N, C))
+        if base is not None and base.data_ptr() != out.data_ptr() and \
+                abs(base.data_ptr() - out.data_ptr()) < 4 * out.numel():
+            raise ValueError("base may be out itself, but must not overlap it otherwise")
+    workspace = _header_workspace(workspace, dev, stream)
+    _enqueue("moe_grouped_mm_wgrad", dev, stream, (dy, x, offsets, base, out, workspace), dy.data_ptr(),
+             x.data_ptr(), offsets.data_ptr(), rows, N, C, E, _OTYPE[dt], _at(base), out.data_ptr(),
+             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def _rows_args(row_weights, n_rows, rows):
+    if row_weights is not None:
+        _want("row_weights", row_weights, torch.float32, (rows,))
+    if n_rows is not None and (n_rows.dtype != torch.int32 or n_rows.numel() != 1):
+        raise TypeError("n_rows must be one int32 on the device")
+
+
+def moe_swiglu_checkpoint(gate_up, row_weights=None, n_rows=None, h=None, codes=None, scale=None, stream=None):
+    """h = bf16(p * silu(g) * u) of gate_up [rows, 2F] bf16 (g | u) and row_weights p [rows] fp32, and its 8-bit
+    checkpoint: codes [rows, 2F] uint8 (E4M3), scale [rows, 2F/128] fp32.  n_rows (one int32 on the device, e.g.
+    offsets[-1:]): only the first n_rows rows are processed.  Returns (h, codes, scale)."""
+    if gate_up.dim() != 2 or gate_up.shape[1] % 256:
+        raise ValueError("gate_up must be [rows, 2F] with F a multiple of 128")
+    rows, F = gate_up.shape[0], gate_up.shape[1] // 2
+    _want("gate_up", gate_up, torch.bfloat16, (rows, 2 * F))
+    _rows_args(row_weights, n_rows, rows)
+    dev = _one_device(gate_up, row_weights, n_rows, h, codes, scale)
+    if h is None:
+        h = _new((rows, F), torch.bfloat16, dev, stream)
+    else:
+        _want("h", h, torch.bfloat16, (rows, F))
+    if codes is None:
+        codes = _new((rows, 2 * F), torch.uint8, dev, stream)
+    else:
+        _codes("codes", codes, (rows, 2 * F))
+    if scale is None:
+        scale = _new((rows, F // 64), torch.float32, dev, stream)
+    else:
+        _want("scale", scale, torch.float32, (rows, F // 64))
+    _enqueue("moe_swiglu_checkpoint", dev, stream, (gate_up, row_weights, n_rows, h, codes, scale),
+             gate_up.data_ptr(), _at(row_weights), _at(n_rows), rows, F, h.data_ptr(), codes.data_ptr(),
+             scale.data_ptr())
+    return h, codes, scale
+
+
+def moe_swiglu_checkpoint_backward(codes, scale, dh, row_weights=None, n_rows=None, dgate_up=None, h=None,
+                                   drow_weights=None, want_h=True, want_drow_weights=True, stream=None):
+    """Gradients of moe_swiglu_checkpoint from its checkpoint: dh [rows, F] bf16 is the gradient of the down
+    product's input taken before the row weight p.  Returns (dgate_up [rows, 2F] bf16, h [rows, F] bf16
+    recomputed for the down weights' gradient, drow_weights [rows] fp32); want_h / want_drow_weights False
+    leave those out (None)."""
+    if dh.dim() != 2 or dh.shape[1] % 128:
+        raise ValueError("dh must be [rows, F] with F a multiple of 128")
+    rows, F = dh.shape
+    _want("dh", dh, torch.bfloat16, (rows, F))
+    _codes("codes", codes, (rows, 2 * F))
+    _want("scale", scale, torch.float32, (rows, F // 64))
+    _rows_args(row_weights, n_rows, rows)
+    dev = _one_device(dh, codes, scale, row_weights, n_rows, dgate_up, h, drow_weights)
+    if dgate_up is None:
+        dgate_up = _new((rows, 2 * F), torch.bfloat16, dev, stream)
+    else:
+        _want("dgate_up", dgate_up, torch.bfloat16, (rows, 2 * F))
+    if h is not None:
+        _want("h", h, torch.bfloat16, (rows, F))
+    elif want_h:
+        h = _new((rows, F), torch.bfloat16, dev, stream)
+    if drow_weights is not None:
+        _want("drow_weights", drow_weights, torch.float32, (rows,))
+    elif want_drow_weights:
+        drow_weights = _new((rows,), torch.float32, dev, stream)
+    _enqueue("moe_swiglu_checkpoint_backward", dev, stream,
+             (codes, scale, dh, row_weights, n_rows, dgate_up, h, drow_weights), codes.data_ptr(), scale.data_ptr(),
+             dh.data_ptr(), _at(row_weights), _at(n_rows), rows, F, dgate_up.data_ptr(), _at(h), _at(drow_weights))
+    return dgate_up, h, drow_weights
+
+
+def moe_permute_rows(x, inv, top_k_weights=None, x_scale=None, out=None, row_weights=None, stream=None):
+    """Rows in expert order: out[inv[t,k]] = x[t] (and row_weights[inv[t,k]] = top_k_weights[t,k]).
+    x [T, H] bf16, or E4M3 codes with x_scale [T, H/128]; inv [T, K] int32, negative = no row.
+    out [n_rows, H] bf16 (default n_rows = T*K; rows no slot names are not written).
+    Returns out, or (out, row_weights) with top_k_weights."""
+    if x.dim() != 2 or inv.dim() != 2:
+        raise ValueError("x must be [T, H] and inv [T, K]")
+    T, H = x.shape
+    K = inv.shape[1]
+    _want("inv", inv, torch.int32, (T, K))
+    if x_scale is None:
+        _want("x", x, torch.bfloat16, (T, H))
+    else:
+        _codes("x", x, (T, H))
+        _want("x_scale", x_scale, torch.float32, (T, H // 128))
+    if top_k_weights is not None:
+        _want("top_k_weights", top_k_weights, torch.float32, (T, K))
+    elif row_weights is not None:
+        raise ValueError("row_weights needs top_k_weights")
+    dev = _one_device(x, inv, top_k_weights, x_scale, out, row_weights)
+    n_rows = T * K if out is None else out.shape[0]
+    if out is None:
+        out = _new((n_rows, H), torch.bfloat16, dev, stream)
+    else:
+        _want("out", out, torch.bfloat16, (n_rows, H))
+    if top_k_weights is not None:
+        if row_weights is None:
+            row_weights = _new((n_rows,), torch.float32, dev, stream)
+        else:
+            _want("row_weights", row_weights, torch.float32, (n_rows,))
+    _enqueue("moe_permute_rows", dev, stream, (x, inv, top_k_weights, x_scale, out, row_weights), x.data_ptr(),
+             _at(x_scale), inv.data_ptr(), _at(top_k_weights), K, T, H, n_rows, out.data_ptr(), _at(row_weights))
+    return out if row_weights is None else (out, row_weights)
+
+
+def moe_unpermute_rows(y, inv, residual=None, drow_weights=None, out=None, dtop_k_weights=None, stream=None):
+    """out [T, H] bf16 = sum over k ascending of y[inv[t,k]] (+ residual[t]), rounded once; with drow_weights
+    [n_rows] fp32 also dtop_k_weights [T, K] = drow_weights[inv[t,k]].  y [n_rows, H] bf16 or fp32; slots whose
+    inv is outside [0, n_rows) count as zero.  Returns out, or (out, dtop_k_weights)."""
+    if y.dim() != 2 or inv.dim() != 2:
+        raise ValueError("y must be [n_rows, H] and inv [T, K]")
+    n_rows, H = y.shape
+    T, K = inv.shape
+    if y.dtype not in _OTYPE:
+        raise TypeError("y must be bf16 or fp32, got %s" % y.dtype)
+    _want("inv", inv, torch.int32, (T, K))
+    if residual is not None:
+        _want("residual", residual, torch.bfloat16, (T, H))
+    if drow_weights is not None:
+        _want("drow_weights", drow_weights, torch.float32, (n_rows,))
+    elif dtop_k_weights is not None:
+        raise ValueError("dtop_k_weights needs drow_weights")
+    dev = _one_device(y, inv, residual, drow_weights, out, dtop_k_weights)
+    if out is None:
+        out = _new((T, H), torch.bfloat16, dev, stream)
+    else:
+        _want("out", out, torch.bfloat16, (T, H))
+    if drow_weights is not None:
+        if dtop_k_weights is None:
+            dtop_k_weights = _new((T, K), torch.float32, dev, stream)
+        else:
+            _want("dtop_k_weights", dtop_k_weights, torch.float32, (T, K))
+    _enqueue("moe_unpermute_rows", dev, stream, (y, inv, residual, drow_weights, out, dtop_k_weights), y.data_ptr(),
+             _OTYPE[y.dtype], inv.data_ptr(), _at(residual), _at(drow_weights), K, T, H, n_rows, out.data_ptr(),
+             _at(dtop_k_weights))
+    return out if drow_weights is None else (out, dtop_k_weights)

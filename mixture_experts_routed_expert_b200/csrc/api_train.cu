@@ -1,0 +1,129 @@
+// api_train.cu -- the C ABI of the training step's operators (declared in
+// include/moe_b200.h): host-side validation and dispatch to the kernels.
+// Nothing here allocates device memory or waits for the device.
+#include "internal.h"
+
+using namespace moe;
+
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+moe_status_t from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return MOE_OK;
+    cudaGetLastError();  // clear a sticky launch error so later calls can proceed
+    return e == cudaErrorInvalidValue ? MOE_ERR_INVALID_ARG : MOE_ERR_CUDA;
+}
+
+constexpr int kMaxRows = 1 << 27;
+
+// Sizes and output type of the three grouped products.
+moe_status_t check_mm(int rows, int N, int C, int E, moe_otype_t ot) {
+    if (rows < 0 || rows > kMaxRows || N < 8 || N % 8 || N > 65536 || C < 8 || C % 8 || C > 65536 || E < 1 ||
+        E > 1024 || (ot != MOE_OUT_BF16 && ot != MOE_OUT_FP32))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+bool workspace_ok(const void *ws, size_t bytes) {
+    return ws && bytes >= kWorkspaceHeaderBytes && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0;
+}
+
+moe_status_t run_mm(const void *x, const int32_t *offsets, const void *w, int rows, int N, int C, int E,
+                    moe_otype_t ot, void *y, void *workspace, size_t workspace_bytes, void *stream, bool transpose) {
+    const moe_status_t s = check_mm(rows, N, C, E, ot);
+    if (s != MOE_OK || rows == 0) return s;
+    if (!x || !offsets || !w || !y || !aligned16(x) || !aligned4(offsets) || !aligned16(w) || !aligned16(y))
+        return MOE_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes)) return MOE_ERR_WORKSPACE;
+    return from_cuda(launch_grouped_mm(x, w, offsets, rows, N, C, E, transpose, ot == MOE_OUT_BF16, y,
+                                       static_cast<int32_t *>(workspace), (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_grouped_mm(const void *x, const int32_t *offsets, const void *w, int rows, int N, int C, int E,
+                            moe_otype_t out_type, void *y, void *workspace, size_t workspace_bytes, void *stream) {
+    return run_mm(x, offsets, w, rows, N, C, E, out_type, y, workspace, workspace_bytes, stream, false);
+}
+
+moe_status_t moe_grouped_mm_dgrad(const void *dy, const int32_t *offsets, const void *w, int rows, int N, int C,
+                                  int E, moe_otype_t out_type, void *dx, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+    return run_mm(dy, offsets, w, rows, N, C, E, out_type, dx, workspace, workspace_bytes, stream, true);
+}
+
+moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, const int32_t *offsets, int rows, int N, int C,
+                                  int E, moe_otype_t out_type, const float *base, void *dw, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    const moe_status_t s = check_mm(rows, N, C, E, out_type);
+    if (s != MOE_OK) return s;
+    if (!dw || !aligned16(dw) || (base && (out_type != MOE_OUT_FP32 || !aligned16(base)))) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (rows == 0) {   // every sum is empty: zeros, or the base
+        const size_t n = (size_t)E * N * C;
+        if (!base) return from_cuda(cudaMemsetAsync(dw, 0, n * (out_type == MOE_OUT_BF16 ? 2 : 4), st));
+        return base == dw ? MOE_OK : from_cuda(cudaMemcpyAsync(dw, base, n * 4, cudaMemcpyDeviceToDevice, st));
+    }
+    if (!dy || !x || !offsets || !aligned16(dy) || !aligned16(x) || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes)) return MOE_ERR_WORKSPACE;
+    return from_cuda(launch_grouped_wgrad(dy, x, offsets, rows, N, C, E, out_type == MOE_OUT_BF16, base, dw,
+                                          static_cast<int32_t *>(workspace), st));
+}
+
+moe_status_t moe_swiglu_checkpoint(const void *gate_up, const float *row_weights, const int32_t *n_rows, int rows,
+                                   int F, void *h, void *codes, float *scale, void *stream) {
+    if (rows < 0 || rows > kMaxRows || F < 128 || F % 128 || F > 16384) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!gate_up || !h || !codes || !scale || !aligned16(gate_up) || !aligned16(h) || !aligned16(codes) ||
+        !aligned4(scale) || !aligned4(row_weights) || !aligned4(n_rows))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_swiglu_checkpoint(gate_up, row_weights, n_rows, rows, F, h, codes, scale,
+                                              (cudaStream_t)stream));
+}
+
+moe_status_t moe_swiglu_checkpoint_backward(const void *codes, const float *scale, const void *dh,
+                                            const float *row_weights, const int32_t *n_rows, int rows, int F,
+                                            void *dgate_up, void *h, float *drow_weights, void *stream) {
+    if (rows < 0 || rows > kMaxRows || F < 128 || F % 128 || F > 16384) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!codes || !scale || !dh || !dgate_up || !aligned16(codes) || !aligned4(scale) || !aligned16(dh) ||
+        !aligned16(dgate_up) || !aligned16(h) || !aligned4(row_weights) || !aligned4(n_rows) ||
+        !aligned4(drow_weights))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_swiglu_checkpoint_backward(codes, scale, dh, row_weights, n_rows, rows, F, dgate_up, h,
+                                                       drow_weights, (cudaStream_t)stream));
+}
+
+moe_status_t moe_permute_rows(const void *x, const float *x_scale, const int32_t *inv, const float *top_k_weights,
+                              int top_k, int T, int H, int n_rows, void *rows, float *row_weights, void *stream) {
+    if (T < 0 || T > (1 << 24) || top_k < 1 || top_k > 16 || H < 8 || H % 8 || H > 65536 || n_rows < 0 ||
+        n_rows > kMaxRows || (x_scale && H % 128))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0 || n_rows == 0) return MOE_OK;
+    if (!x || !inv || !rows || !aligned16(x) || !aligned4(x_scale) || !aligned4(inv) || !aligned16(rows) ||
+        !aligned4(top_k_weights) || !aligned4(row_weights) || !top_k_weights != !row_weights)
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_permute_rows(x, x_scale, inv, top_k_weights, T, top_k, H, n_rows, rows, row_weights,
+                                         (cudaStream_t)stream));
+}
+
+moe_status_t moe_unpermute_rows(const void *y, moe_otype_t y_type, const int32_t *inv, const void *residual,
+                                const float *drow_weights, int top_k, int T, int H, int n_rows, void *out,
+                                float *dtop_k_weights, void *stream) {
+    if (T < 0 || T > (1 << 24) || top_k < 1 || top_k > 16 || H < 8 || H % 8 || H > 65536 || n_rows < 0 ||
+        n_rows > kMaxRows || (y_type != MOE_OUT_BF16 && y_type != MOE_OUT_FP32))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((n_rows > 0 && !y) || !inv || !out || !aligned16(y) || !aligned4(inv) || !aligned16(residual) ||
+        !aligned16(out) || !aligned4(drow_weights) || !aligned4(dtop_k_weights) ||
+        (n_rows > 0 && !drow_weights && dtop_k_weights) || (drow_weights && !dtop_k_weights))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_unpermute_rows(y, y_type == MOE_OUT_FP32, inv, residual, drow_weights, T, top_k, H, n_rows,
+                                           out, dtop_k_weights, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -162,6 +162,25 @@ cudaError_t launch_route(const float *logits, const float *bias, int64_t T, int 
                          int topk_group, int top_k, float scale, int32_t *idx, float *w,
                          int32_t *offsets, cudaStream_t st);
 
+// ---- the training step's operators (C = input features, N = output features) ----
+// y = x w^T per expert (x [rows][C]), or, transposed, dx = dy w (x = dy [rows][N]).
+cudaError_t launch_grouped_mm(const void *x, const void *w, const int32_t *offsets, int rows, int N, int C, int E,
+                              bool transpose, bool out_bf16, void *out, int32_t *status, cudaStream_t st);
+// dw = (base +) dy^T x per expert; base (fp32 output only) may be dw itself.
+cudaError_t launch_grouped_wgrad(const void *dy, const void *x, const int32_t *offsets, int rows, int N, int C, int E,
+                                 bool out_bf16, const float *base, void *dw, int32_t *status, cudaStream_t st);
+// n_rows: device count of the rows to process (clamped to [0, rows]), or null for all.
+cudaError_t launch_swiglu_checkpoint(const void *gu, const float *weight, const int32_t *n_rows, int rows, int F,
+                                     void *h, void *codes, float *scale, cudaStream_t st);
+cudaError_t launch_swiglu_checkpoint_backward(const void *codes, const float *scale, const void *dh,
+                                              const float *weight, const int32_t *n_rows, int rows, int F, void *dgu,
+                                              void *h, float *dweight, cudaStream_t st);
+cudaError_t launch_permute_rows(const void *x, const float *x_scale, const int32_t *inv, const float *weights,
+                                int64_t T, int K, int H, int n_out, void *out, float *row_weights, cudaStream_t st);
+cudaError_t launch_unpermute_rows(const void *y, bool y_fp32, const int32_t *inv, const void *residual,
+                                  const float *drow, int64_t T, int K, int H, int n_in, void *out, float *dweights,
+                                  cudaStream_t st);
+
 // cudaLaunchKernelEx with optional programmatic dependent launch.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,

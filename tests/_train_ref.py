@@ -1,0 +1,118 @@
+"""Plain 64-bit statements of the training step's operators (numpy-like torch
+code on the CPU) and the tolerances their tests use."""
+import torch
+
+BF16_HALF = 2.0 ** -8      # half a bf16 step, relative to the value
+F32_STEP = 2.0 ** -23
+
+
+def offsets_of(counts, first=0):
+    o = [first]
+    for c in counts:
+        o.append(o[-1] + c)
+    return torch.tensor(o, dtype=torch.int32)
+
+
+def spans(offsets, rows):
+    """(expert, first row, end) with the documented clamping."""
+    out = []
+    o = offsets.tolist()
+    for e in range(len(o) - 1):
+        b = min(max(o[e], 0), rows)
+        out.append((e, b, min(max(o[e + 1], b), rows)))
+    return out
+
+
+def mm64(x, offsets, w, transpose):
+    """(result, sum of |products|) in 64 bits, zero rows where no expert owns them."""
+    x, w = x.double(), w.double()
+    rows, co = x.shape[0], w.shape[2 if transpose else 1]
+    y, s = torch.zeros(rows, co, dtype=torch.float64), torch.zeros(rows, co, dtype=torch.float64)
+    for e, a, b in spans(offsets, rows):
+        m = w[e] if transpose else w[e].t()
+        y[a:b], s[a:b] = x[a:b] @ m, x[a:b].abs() @ m.abs()
+    return y, s
+
+
+def wgrad64(dy, x, offsets, base=None):
+    dy, x = dy.double(), x.double()
+    E = len(offsets) - 1
+    y = torch.zeros(E, dy.shape[1], x.shape[1], dtype=torch.float64)
+    s = torch.zeros_like(y)
+    for e, a, b in spans(offsets, x.shape[0]):
+        y[e], s[e] = dy[a:b].t() @ x[a:b], dy[a:b].abs().t() @ x[a:b].abs()
+    if base is not None:
+        y, s = y + base.double(), s + base.double().abs()
+    return y, s
+
+
+def check_sum(got, ref, mag, terms, what=""):
+    """got against a 64-bit sum of `terms` fp32-accumulated products whose
+    absolute values add up to `mag`: each of the terms + 2 additions is off by
+    at most one fp32 step of a partial sum, which is at most mag (the tensor
+    cores may truncate, hence a step and not half of one); a bf16 result adds
+    half a bf16 step of its own value."""
+    tol = (terms + 2) * F32_STEP * mag
+    if got.dtype == torch.bfloat16:
+        tol = tol + BF16_HALF * (ref.abs() + tol)
+    g = got.double().cpu()
+    assert g.shape == ref.shape
+    assert torch.isfinite(g).all(), "%s: non-finite" % what
+    off = (g - ref).abs()
+    assert not (off > tol).any(), "%s: %d off, worst %.3e of the tolerance" % (
+        what, int((off > tol).sum()), float((off / tol.clamp_min(1e-300)).max()))
+
+
+# ------------------------------------------------- 8-bit block-128 values --
+def quantize64(v):
+    """Codes (as E4M3 values, fp64) and power-of-two scales per 128 columns."""
+    blk = v.double().unflatten(-1, (-1, 128))
+    amax = blk.abs().amax(-1)
+    m, e = torch.frexp(amax)
+    k = torch.where(amax == 0, torch.zeros_like(e), e - 9 + (m > 0.875)).clamp(-127, 127)
+    scale = torch.exp2(k.double())
+    q = blk / scale.unsqueeze(-1)
+    _, qe = torch.frexp(q)
+    step = torch.exp2((qe - 4).clamp_min(-9).double())
+    q = torch.round(q / step) * step
+    return q.flatten(-2), scale
+
+
+def restore64(codes, scale):
+    """codes: uint8 E4M3 bytes."""
+    v = codes.view(torch.float8_e4m3fn).double().unflatten(-1, (-1, 128))
+    return (v * scale.double().unsqueeze(-1)).flatten(-2)
+
+
+def swiglu64(gu, p=None):
+    g, u = gu.double().chunk(2, -1)
+    h = g * torch.sigmoid(g) * u
+    return h if p is None else h * p.double().unsqueeze(-1)
+
+
+def swiglu_backward64(gu, dh, p=None):
+    """(dgate_up, h, drow) by the formula."""
+    g, u = gu.double().chunk(2, -1)
+    dh = dh.double()
+    s = torch.sigmoid(g)
+    a = g * s
+    q = torch.ones(gu.shape[0], 1, dtype=torch.float64) if p is None else p.double().unsqueeze(-1)
+    return torch.cat([q * dh * u * (s + a * torch.sigmoid(-g)), q * dh * a], -1), q * a * u, (dh * a * u).sum(-1)
+
+
+def expert_order(idx, E):
+    """counts, offsets [E+1], inv [T,K] of a routing, by plain loops."""
+    T, K = idx.shape
+    buckets = [[] for _ in range(E)]
+    for s, e in enumerate(idx.reshape(-1).tolist()):
+        if 0 <= e < E:
+            buckets[e].append(s)
+    inv = torch.full((T * K,), -1, dtype=torch.int32)
+    at = 0
+    off = [0]
+    for b in buckets:
+        for s in b:
+            inv[s] = at
+            at += 1
+        off.append(at)
+    return torch.tensor(off, dtype=torch.int32), inv.view(T, K)

@@ -1,0 +1,184 @@
+"""The grouped products (forward, input gradient, weight gradient) against a
+64-bit plain form, at the sizes, offsets and values where they can go wrong."""
+import pytest
+import torch
+
+from _train_ref import check_sum, mm64, offsets_of, spans, wgrad64
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_routed_expert_b200 as m
+    return m
+
+
+def _inputs(counts, N, C, first=0, slack=0, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    off = offsets_of(counts, first)
+    rows = int(off[-1]) + slack
+    x = torch.randn(rows, C, generator=g).to(BF)
+    dy = torch.randn(rows, N, generator=g).to(BF)
+    w = (torch.randn(len(counts), N, C, generator=g) * 0.1).to(BF)
+    return off, x, dy, w
+
+
+CASES = [
+    ([1], 8, 8),                              # the smallest
+    ([3, 0, 1], 8, 72),
+    ([0, 5, 0, 17, 1, 300, 0], 72, 200),      # empty experts, edges inside every tile
+    ([64, 128, 256, 257, 15, 16, 17], 128, 64),
+    ([100, 33, 512], 136, 1288),
+    ([700], 264, 520),                        # one expert, several row tiles
+    ([2, 1, 0, 1, 2], 1792, 1280),            # a token or two per expert
+    ([0, 0, 0], 64, 64),                      # nobody has rows
+]
+
+
+@pytest.mark.parametrize("counts,N,C", CASES)
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_products(moe, cuda_dev, counts, N, C, dt):
+    off, x, dy, w = _inputs(counts, N, C)
+    d = [t.to(cuda_dev) for t in (off, x, dy, w)]
+    rows = x.shape[0]
+    y = moe.moe_grouped_mm(d[1], d[0], d[3], out_dtype=dt)
+    dx = moe.moe_grouped_mm_dgrad(d[2], d[0], d[3], out_dtype=dt)
+    dw = moe.moe_grouped_mm_wgrad(d[2], d[1], d[0], out_dtype=dt)
+    assert y.shape == (rows, N) and dx.shape == (rows, C) and y.dtype == dx.dtype == dw.dtype == dt
+    check_sum(y, *mm64(x, off, w, False), C, "forward")
+    check_sum(dx, *mm64(dy, off, w, True), N, "input gradient")
+    check_sum(dw, *wgrad64(dy, x, off), max(counts), "weight gradient")
+
+
+def test_rows_of_nobody(moe, cuda_dev):
+    """Rows before the first expert and behind the last keep their contents,
+    and what they hold (NaN, infinities) reaches no sum."""
+    off, x, dy, w = _inputs([5, 0, 70, 19], 72, 136, first=7, slack=30, seed=1)
+    own = slice(7, 101)
+    xs, ds = x.clone(), dy.clone()
+    for t in (xs, ds):
+        t[:7], t[101:] = float("nan"), float("inf")
+    o, xd, dd, wd = (t.to(cuda_dev) for t in (off, xs, ds, w))
+    for dt in (BF, F32):
+        y = torch.full((131, 72), -3.0, dtype=dt, device=cuda_dev)
+        dx = torch.full((131, 136), -3.0, dtype=dt, device=cuda_dev)
+        moe.moe_grouped_mm(xd, o, wd, out=y)
+        moe.moe_grouped_mm_dgrad(dd, o, wd, out=dx)
+        dw = moe.moe_grouped_mm_wgrad(dd, xd, o, out_dtype=dt)
+        for t in (y, dx):
+            assert (t[:7] == -3).all() and (t[101:] == -3).all()
+        ry, my = mm64(x, off, w, False)
+        rx, mx = mm64(dy, off, w, True)
+        check_sum(y[own], ry[own], my[own], 136, "forward")
+        check_sum(dx[own], rx[own], mx[own], 72, "input gradient")
+        x0, d0 = x.clone(), dy.clone()
+        for t in (x0, d0):
+            t[:7], t[101:] = 0, 0
+        check_sum(dw, *wgrad64(d0, x0, off), 70, "weight gradient")
+
+
+def test_neighbours_do_not_leak(moe, cuda_dev):
+    """Infinities and NaN of one expert (its rows or its weights) stay its own:
+    the tiles of the experts beside it read them and must not use them."""
+    counts = [21, 40, 9]
+    off, x, dy, w = _inputs(counts, 72, 104, seed=2)
+    xs, ds, ws = x.clone(), dy.clone(), w.clone()
+    xs[21:61], ds[21:61], ws[1] = float("inf"), float("nan"), float("inf")
+    o, xd, dd, wd = (t.to(cuda_dev) for t in (off, xs, ds, ws))
+    y = moe.moe_grouped_mm(xd, o, wd)
+    dx = moe.moe_grouped_mm_dgrad(dd, o, wd)
+    dw = moe.moe_grouped_mm_wgrad(dd, xd, o)
+    ry, my = mm64(x, off, w, False)
+    rx, mx = mm64(dy, off, w, True)
+    rw, mw = wgrad64(dy, x, off)
+    for e, a, b in spans(off, 70):
+        if e == 1:
+            assert not torch.isfinite(y[a:b]).any() and torch.isnan(dx[a:b]).all() and torch.isnan(dw[e]).all()
+        else:
+            check_sum(y[a:b], ry[a:b], my[a:b], 104, "forward %d" % e)
+            check_sum(dx[a:b], rx[a:b], mx[a:b], 72, "input gradient %d" % e)
+            check_sum(dw[e], rw[e], mw[e], counts[e], "weight gradient %d" % e)
+
+
+def test_offsets_outside_the_rows_are_clamped(moe, cuda_dev):
+    off = torch.tensor([-5, 10, 4000], dtype=torch.int32)
+    _, x, dy, _ = _inputs([20], 40, 72, seed=3)
+    w = (torch.randn(2, 40, 72, generator=torch.Generator().manual_seed(4)) * 0.1).to(BF)
+    o, xd, dd, wd = (t.to(cuda_dev) for t in (off, x, dy, w))
+    check_sum(moe.moe_grouped_mm(xd, o, wd), *mm64(x, off, w, False), 72)
+    check_sum(moe.moe_grouped_mm_dgrad(dd, o, wd), *mm64(dy, off, w, True), 40)
+    check_sum(moe.moe_grouped_mm_wgrad(dd, xd, o), *wgrad64(dy, x, off), 10)
+
+
+def test_many_experts(moe, cuda_dev):
+    counts = [(7 * e) % 3 for e in range(1024)]
+    off, x, dy, w = _inputs(counts, 16, 24, seed=5)
+    o, xd, dd, wd = (t.to(cuda_dev) for t in (off, x, dy, w))
+    check_sum(moe.moe_grouped_mm(xd, o, wd, out_dtype=F32), *mm64(x, off, w, False), 24)
+    check_sum(moe.moe_grouped_mm_dgrad(dd, o, wd, out_dtype=F32), *mm64(dy, off, w, True), 16)
+    check_sum(moe.moe_grouped_mm_wgrad(dd, xd, o, out_dtype=F32), *wgrad64(dy, x, off), 2)
+
+
+@pytest.mark.parametrize("counts", [[130, 0, 65], [0, 0, 3], [0, 0, 0]])
+def test_base_is_added(moe, cuda_dev, counts):
+    off, x, dy, _ = _inputs(counts, 72, 136, seed=6)
+    base = torch.randn(3, 72, 136, generator=torch.Generator().manual_seed(7))
+    o, xd, dd, bd = (t.to(cuda_dev) for t in (off, x, dy, base))
+    ref, mag = wgrad64(dy, x, off, base)
+    dw = moe.moe_grouped_mm_wgrad(dd, xd, o, base=bd)
+    check_sum(dw, ref, mag, max(counts) + 1, "new tensor")
+    assert torch.equal(bd.cpu(), base)
+    assert moe.moe_grouped_mm_wgrad(dd, xd, o, base=bd, out=bd) is bd
+    assert torch.equal(bd, dw)
+
+
+def test_no_rows_at_all(moe, cuda_dev):
+    o = torch.zeros(4, dtype=torch.int32, device=cuda_dev)
+    x = torch.empty(0, 64, dtype=BF, device=cuda_dev)
+    dy = torch.empty(0, 32, dtype=BF, device=cuda_dev)
+    w = torch.zeros(3, 32, 64, dtype=BF, device=cuda_dev)
+    assert moe.moe_grouped_mm(x, o, w).shape == (0, 32)
+    assert moe.moe_grouped_mm_dgrad(dy, o, w).shape == (0, 64)
+    for dt in (BF, F32):
+        dw = torch.full((3, 32, 64), 5.0, dtype=dt, device=cuda_dev)
+        assert (moe.moe_grouped_mm_wgrad(dy, x, o, out=dw) == 0).all()
+    base = torch.randn(3, 32, 64, device=cuda_dev)
+    assert torch.equal(moe.moe_grouped_mm_wgrad(dy, x, o, base=base), base)
+
+
+def test_same_bits_graph_and_streams(moe, cuda_dev):
+    """Equal bits from repeated calls, from two streams that share a workspace,
+    and from a captured graph replayed on new inputs; the status stays clean."""
+    off, x, dy, w = _inputs([40, 0, 300, 11, 129], 200, 328, seed=8)
+    o, xd, dd, wd = (t.to(cuda_dev) for t in (off, x, dy, w))
+    ws = torch.zeros(8192, dtype=torch.uint8, device=cuda_dev)
+
+    def call(stream=None):
+        return (moe.moe_grouped_mm(xd, o, wd, workspace=ws, stream=stream),
+                moe.moe_grouped_mm_dgrad(dd, o, wd, workspace=ws, stream=stream),
+                moe.moe_grouped_mm_wgrad(dd, xd, o, out_dtype=F32, workspace=ws, stream=stream))
+
+    first = call()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    both = [call(s) for s in (s1, s2) for _ in range(3)]
+    torch.cuda.synchronize()
+    for outs in both:
+        for a, b in zip(first, outs):
+            assert torch.equal(a, b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        caught = call()
+    xd.copy_(xd.flip(0))
+    dd.copy_(dd.flip(0))
+    o.copy_(offsets_of([11, 129, 0, 40, 300]))
+    g.replay()
+    torch.cuda.synchronize()
+    again = call()
+    torch.cuda.synchronize()
+    for a, b in zip(caught, again):
+        assert torch.equal(a, b)
+    assert moe.moe_workspace_status(ws) == 0

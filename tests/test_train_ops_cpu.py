@@ -1,0 +1,136 @@
+"""Refusals of the training step's operators: the library's host checks on bare
+pointers and the binding's checks on tensors (no GPU needed: both happen
+before any CUDA call)."""
+import ctypes
+
+import pytest
+import torch
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_routed_expert_b200 as m
+    return m
+
+
+p = ctypes.c_void_p(0x1000)
+q = ctypes.c_void_p(0x1004)          # 4- but not 16-byte aligned
+odd = ctypes.c_void_p(0x1001)
+N = None
+OK, ARG, WORKSPACE = 0, 1, 3
+
+
+@pytest.mark.parametrize("name", ["moe_grouped_mm", "moe_grouped_mm_dgrad"])
+def test_products_host_checks(moe, name):
+    f = getattr(moe.lib, name)
+
+    def call(a=p, off=p, w=p, rows=4, n=64, c=72, e=3, ot=0, y=p, ws=p, size=8192):
+        return f(a, off, w, rows, n, c, e, ot, y, ws, size, N)
+
+    assert call(rows=0, a=N, off=N, w=N, y=N, ws=N, size=0) == OK
+    for bad in (dict(rows=-1), dict(rows=(1 << 27) + 1), dict(n=4), dict(n=60), dict(c=0), dict(c=65544), dict(e=0),
+                dict(e=1025), dict(ot=2), dict(ot=-1), dict(a=N), dict(off=N), dict(w=N), dict(y=N), dict(a=q),
+                dict(w=q), dict(y=q), dict(off=odd)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(ws=N), dict(size=8191), dict(ws=ctypes.c_void_p(0x1010))):
+        assert call(**bad) == WORKSPACE, bad
+
+
+def test_wgrad_host_checks(moe):
+    f = moe.lib.moe_grouped_mm_wgrad
+
+    def call(dy=p, x=p, off=p, rows=4, n=64, c=72, e=3, ot=1, base=N, dw=p, ws=p, size=8192):
+        return f(dy, x, off, rows, n, c, e, ot, base, dw, ws, size, N)
+
+    assert call(rows=0, dy=N, x=N, off=N, base=p, ws=N, size=0) == OK      # accumulated in place: nothing to add
+    for bad in (dict(rows=-1), dict(n=12), dict(c=7), dict(e=0), dict(ot=2), dict(dy=N), dict(x=N), dict(off=N),
+                dict(dw=N), dict(dy=q), dict(x=q), dict(dw=q), dict(base=q), dict(base=p, ot=0), dict(off=odd),
+                dict(rows=0, dw=N)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(ws=N), dict(size=0)):
+        assert call(**bad) == WORKSPACE, bad
+
+
+def test_checkpoint_host_checks(moe):
+    f, b = moe.lib.moe_swiglu_checkpoint, moe.lib.moe_swiglu_checkpoint_backward
+
+    def fwd(gu=p, w=N, n=N, rows=4, F=128, h=p, c=p, s=p):
+        return f(gu, w, n, rows, F, h, c, s, N)
+
+    def bwd(c=p, s=p, dh=p, w=N, n=N, rows=4, F=128, dgu=p, h=N, dw=N):
+        return b(c, s, dh, w, n, rows, F, dgu, h, dw, N)
+
+    assert fwd(rows=0, gu=N, h=N, c=N, s=N) == OK and bwd(rows=0, c=N, s=N, dh=N, dgu=N) == OK
+    for bad in (dict(rows=-1), dict(F=0), dict(F=64), dict(F=200), dict(F=16512), dict(gu=N), dict(h=N), dict(c=N),
+                dict(s=N), dict(gu=q), dict(h=q), dict(c=q), dict(s=odd), dict(w=odd), dict(n=odd)):
+        assert fwd(**bad) == ARG, bad
+    for bad in (dict(rows=-1), dict(F=100), dict(c=N), dict(s=N), dict(dh=N), dict(dgu=N), dict(c=q), dict(dh=q),
+                dict(dgu=q), dict(h=q), dict(dw=odd), dict(w=odd), dict(n=odd), dict(s=odd)):
+        assert bwd(**bad) == ARG, bad
+
+
+def test_rows_host_checks(moe):
+    f, b = moe.lib.moe_permute_rows, moe.lib.moe_unpermute_rows
+
+    def per(x=p, xs=N, inv=p, w=N, k=2, T=4, H=128, n=8, rows=p, rw=N):
+        return f(x, xs, inv, w, k, T, H, n, rows, rw, N)
+
+    def unp(y=p, t=0, inv=p, r=N, d=N, k=2, T=4, H=128, n=8, out=p, dw=N):
+        return b(y, t, inv, r, d, k, T, H, n, out, dw, N)
+
+    assert per(T=0, x=N, inv=N, rows=N) == OK and per(n=0, x=N, rows=N) == OK
+    assert unp(T=0, y=N, inv=N, out=N) == OK
+    for bad in (dict(T=-1), dict(T=(1 << 24) + 1), dict(k=0), dict(k=17), dict(H=4), dict(H=65544), dict(n=-1),
+                dict(xs=p, H=136), dict(x=N), dict(inv=N), dict(rows=N), dict(x=q), dict(rows=q), dict(inv=odd),
+                dict(w=p), dict(rw=p), dict(w=odd, rw=p)):
+        assert per(**bad) == ARG, bad
+    for bad in (dict(T=-1), dict(k=0), dict(H=12), dict(n=-1), dict(t=2), dict(y=N), dict(inv=N), dict(out=N),
+                dict(y=q), dict(r=q), dict(out=q), dict(d=p), dict(dw=p), dict(inv=odd)):
+        assert unp(**bad) == ARG, bad
+
+
+def test_binding_refusals(moe):
+    x, dy = torch.zeros(6, 64, dtype=BF), torch.zeros(6, 32, dtype=BF)
+    w, off = torch.zeros(3, 32, 64, dtype=BF), torch.zeros(4, dtype=I32)
+    mm, dg, wg = moe.moe_grouped_mm, moe.moe_grouped_mm_dgrad, moe.moe_grouped_mm_wgrad
+    for call in (lambda: mm(x, off, w), lambda: dg(dy, off, w), lambda: wg(dy, x, off)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    for call in (lambda: mm(x.float(), off, w), lambda: mm(x, off.long(), w), lambda: mm(x, off, w.half()),
+                 lambda: mm(x, off, w, out_dtype=torch.float16), lambda: mm(x, off, w, out=torch.zeros(6, 32, dtype=I32)),
+                 lambda: mm(x, off, w, out=torch.zeros(6, 32, dtype=BF), out_dtype=F32),
+                 lambda: wg(dy, x, off, base=torch.zeros(3, 32, 64), out_dtype=BF),
+                 lambda: wg(dy, x, off, base=torch.zeros(3, 32, 64, dtype=BF)), lambda: wg(dy.float(), x, off)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: mm(dy, off, w), lambda: dg(x, off, w), lambda: mm(x, off[:3], w), lambda: mm(x, off, w[0]),
+                 lambda: wg(dy[:5], x, off), lambda: wg(dy, x, off.view(2, 2)),
+                 lambda: wg(dy, x, off, base=torch.zeros(3, 32, 56))):
+        with pytest.raises(ValueError):
+            call()
+    gu, dh = torch.zeros(6, 512, dtype=BF), torch.zeros(6, 256, dtype=BF)
+    codes, scale = torch.zeros(6, 512, dtype=torch.uint8), torch.zeros(6, 4)
+    ck, cb = moe.moe_swiglu_checkpoint, moe.moe_swiglu_checkpoint_backward
+    for call in (lambda: ck(gu[:, :384]), lambda: ck(gu, row_weights=torch.zeros(5)), lambda: ck(gu),
+                 lambda: cb(codes, scale[:, :3], dh), lambda: cb(codes[:5], scale, dh), lambda: cb(codes, scale, dh)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: ck(gu.half()), lambda: ck(gu, n_rows=torch.zeros(2, dtype=I32)),
+                 lambda: ck(gu, n_rows=torch.zeros(1, dtype=torch.int64)), lambda: cb(codes.int(), scale, dh),
+                 lambda: cb(codes, scale.double(), dh), lambda: cb(codes, scale, dh.float())):
+        with pytest.raises(TypeError):
+            call()
+    inv = torch.zeros(6, 2, dtype=I32)
+    pe, un = moe.moe_permute_rows, moe.moe_unpermute_rows
+    for call in (lambda: pe(x, inv[:5]), lambda: pe(x, inv, row_weights=torch.zeros(12)), lambda: pe(x, inv),
+                 lambda: pe(x, inv, torch.zeros(6, 3)), lambda: un(x, inv, residual=dy), lambda: un(x, inv),
+                 lambda: un(x, inv, drow_weights=torch.zeros(5)), lambda: un(x, inv, dtop_k_weights=torch.zeros(6, 2)),
+                 lambda: pe(torch.zeros(6, 64, dtype=torch.uint8), inv, x_scale=torch.zeros(6, 1))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: pe(x.float(), inv), lambda: pe(x, inv.long()), lambda: pe(x, inv, x_scale=torch.zeros(6, 1)),
+                 lambda: un(x.half(), inv)):
+        with pytest.raises(TypeError):
+            call()
