@@ -7,9 +7,10 @@
 //   input gradient   dx[r, c]    = sum_n dy[r, n] * w[e, n, c]
 //   weight gradient  dw[e, n, c] = base[e, n, c] + sum_{r of e} dy[r, n] * x[r, c]
 //
-// One kernel serves the three.  Its A operand (MMA M, 128 wide) is the side
-// that is contiguous in the output, its B operand (MMA N, up to 256) the
-// other side, so that the 32 lanes of an epilogue warp always hold 32
+// One kernel serves the three, two CTAs of a cluster on one 256 x 256 tile
+// (cta_group::2): each holds 128 columns of the A operand and half of the B
+// operand, and 128 x 256 of the accumulator.  The A operand (MMA M) is the
+// side that is contiguous in the output, the B operand (MMA N) the other, so that the 32 lanes of an epilogue warp always hold 32
 // neighbouring output columns:
 //   forward          A = w[e]  (reduction contiguous: "K-major")   B = x rows  (K-major)
 //   input gradient   A = w[e]  (output side contiguous: "MN-major") B = dy rows (K-major)
@@ -22,9 +23,13 @@
 // zeros in shared memory, on both operands, before the MMA reads them (a
 // zero on one side alone would let a neighbour's infinity through as NaN).
 //
-// Persistent: one CTA per SM walks the tile list, which every CTA derives
-// from the offsets on the device.  Warp roles: 0 TMA producer, 1 MMA issue,
-// 2-9 epilogue (two warps per TMEM lane quarter, alternating 32 columns).
+// Persistent: one CTA per SM, the pairs walk the tile list, which every CTA
+// derives from the offsets on the device.  Warp roles: 0 TMA producer of the
+// CTA's own operands (both CTAs' copies complete on the leading CTA's
+// barrier); 1 in the leading CTA MMA issue for the pair, in the other idle
+// but for a ragged end, which each CTA zeroes in its own operands before the
+// other CTA's warp tells the leader; 2-9 epilogue (two warps per TMEM lane
+// quarter, alternating 32 columns).
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -38,12 +43,13 @@ namespace {
 enum Op : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
 constexpr int kBK = 64;                        // reduction elements per stage = one 128-byte swizzle row
-constexpr int kBN = 256;                       // B-side width of a tile
-constexpr int kStages = 4;
+constexpr int kTM = 256;                       // A-side width of a pair's tile
+constexpr int kBN = 256;                       // B-side width of a pair's tile
+constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kABytes = kBM * 128;
-constexpr int kBBytes = kBN * 128;
+constexpr int kBBytes = kBN / 2 * 128;         // a CTA holds half of B
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kOutStage = kEpiWarps * 32 * 32 * 2;
@@ -83,6 +89,108 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
     return d;
 }
 
+// ---- the pair: cluster barriers, remote arrivals, cta_group::2 tcgen05 -----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// True in one lane of a converged warp (the same on every call).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// The address of the leading CTA's barrier at the same place as `bar`.
+__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+    return a;
+}
+// Arrive on the leading CTA's barrier; the cluster-scope release (about 2000
+// cycles: every block of a product taking it ran at half the speed) is for
+// shared-memory writes of this thread that the leader's MMAs read.
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_leader_release(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+// TMA tile loads into this CTA's shared memory that complete on a barrier of
+// either CTA of the pair (no multicast).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::"
+        "cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::"
+        "cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+// mbar_wait for arrivals from the other CTA (cluster scope).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t a = smem_u32(bar);
+    long long t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (it == 0) t0 = clock64();
+        if ((it & 255u) == 255u) {
+            if (*abort) return false;
+            if (clock64() - t0 > kWaitLimitCycles) return false;
+        }
+    }
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on `bar` in both CTAs when every MMA issued so far is done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// The same on this CTA's `bar` alone.
+__device__ __forceinline__ void mma_commit_leader(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
 template <int OP>
 __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t *s_beg, const int32_t *s_end,
                                           const int32_t *s_tiles, int MT, int NT) {
@@ -91,7 +199,7 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
         t.e = w / (MT * NT);
         const int local = w - t.e * MT * NT;
         const int n = local / MT;
-        t.m0 = (local - n * MT) * kBM;
+        t.m0 = (local - n * MT) * kTM;
         t.row0 = n * kBN;
         t.nrows = min(kBN, a.N - t.row0);
         t.red0 = s_beg[t.e];
@@ -108,7 +216,7 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
         const int m = local / nt, n = local - m * nt;
         const int n_e = s_end[lo] - s_beg[lo];
         const int rpt = min(kBN, ((n_e + nt - 1) / nt + 15) & ~15);
-        t.m0 = m * kBM;
+        t.m0 = m * kTM;
         t.row0 = s_beg[lo] + n * rpt;
         t.nrows = max(0, min(rpt, n_e - n * rpt));
         t.red0 = 0;
@@ -117,17 +225,27 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
     return t;
 }
 
+// Whether k-block kb ends inside a 16-row step with the next expert's rows in it.
+template <int OP>
+__device__ __forceinline__ bool ragged_end(const MmTile &t, int kb) {
+    const int left = t.red - kb * kBK;
+    return OP == kWgrad && left < kBK && (left & 15);
+}
+
 template <int OP, bool OUT_BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_mm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const MmArgs args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem;
+    // full: the leader's counts both CTAs' copies, but for a ragged end, where
+    // each CTA's own barrier counts its own and `relay` follows
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRingBytes);
     uint64_t *empty = full + kStages;
     uint64_t *tfull = empty + kStages;
-    uint64_t *tempty = tfull + 2;
-    uint64_t *drained = tempty + 2;
+    uint64_t *tempty = tfull + 2;              // the leader's, for both CTAs' epilogues
+    uint64_t *relay = tempty + 2;              // the leader's: the other CTA's ragged end is zeroed
+    uint64_t *drained = relay + kStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int32_t *s_part = reinterpret_cast<int32_t *>(tmem_slot + 2);          // [kThreads / 32]
@@ -137,14 +255,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t *s_tiles = s_end + args.E;                                      // [E+1]
 
     const int warp = threadIdx.x >> 5, lane = lane_id();
+    const int rank = (int)cluster_rank();      // 0: the leader
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&relay[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], 32 * kEpiWarps);
+            mbar_init(&tempty[a], 2 * kEpiWarps);
         }
         mbar_init(drained, 1);
         *abort_flag = 0;
@@ -152,10 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
     pdl_wait();
     // Row ranges of the experts, clamped into the matrices whatever the
     // offsets hold, and the prefix sum of their row tiles: each thread sums a
@@ -187,9 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == kThreads - 1) s_tiles[args.E] = before;
     tc_fence_before();
     __syncthreads();
+    __syncwarp();
+    cluster_sync();                            // both CTAs' barriers and TMEM are ready
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int MT = (args.M + kBM - 1) / kBM;
+    const int MT = (args.M + kTM - 1) / kTM;
     const int NT = (args.N + kBN - 1) / kBN;
     const int total = OP == kWgrad ? args.E * MT * NT : s_tiles[args.E] * MT;
     pdl_launch_dependents();
@@ -204,106 +324,143 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int s = 0; s < kStages; ++s) armed[s] = -1;
             bool ok = true;
-            for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            for (int w = pair; w < total && ok; w += pairs) {
                 const MmTile t = mm_tile<OP>(w, args, s_beg, s_end, s_tiles, MT, NT);
                 if (t.nrows == 0) continue;
                 const int KB = (t.red + kBK - 1) / kBK;
-                const int nbox = OP == kWgrad ? (t.nrows + 63) / 64 : (t.nrows + args.box_rows - 1) / args.box_rows;
+                const int half = ((t.nrows + 15) & ~15) / 2;         // B rows of each CTA
+                const int m0 = t.m0 + rank * kBM, row0 = t.row0 + rank * half;
+                const int nbox = OP == kWgrad ? (half + 63) / 64 : (half + args.box_rows - 1) / args.box_rows;
                 const int box_bytes = OP == kWgrad ? kChunkBytes : args.box_rows * 128;
+                const uint32_t bytes = kABytes + nbox * box_bytes;
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
                     uint8_t *sA = ring + stage * kStageBytes;
                     uint8_t *sB = sA + kABytes;
-                    mbar_arrive_expect_tx(&full[stage], kABytes + nbox * box_bytes);
-                    armed[stage] = (int)phase;
+                    const bool ragged = ragged_end<OP>(t, kb);
+                    if (rank == 0 || ragged) mbar_arrive_expect_tx(&full[stage], ragged ? bytes : 2 * bytes);
+                    if (rank == 0) armed[stage] = (int)phase;
+                    const uint32_t bar = ragged ? smem_u32(&full[stage]) : leader_addr(&full[stage]);
                     const int k0 = t.red0 + kb * kBK;
                     if (OP == kFwd) {
-                        tma_load_3d(sA, &tmA, &full[stage], k0, t.m0, t.e, pol);
+                        tma_load_3d_pair(sA, &tmA, bar, k0, m0, t.e, pol);
                     } else {
                         for (int c = 0; c < kBM / 64; ++c) {
                             if (OP == kDgrad)
-                                tma_load_3d(sA + c * kChunkBytes, &tmA, &full[stage], t.m0 + 64 * c, k0, t.e, pol);
+                                tma_load_3d_pair(sA + c * kChunkBytes, &tmA, bar, m0 + 64 * c, k0, t.e, pol);
                             else
-                                tma_load_2d(sA + c * kChunkBytes, &tmA, &full[stage], t.m0 + 64 * c, k0, pol);
+                                tma_load_2d_pair(sA + c * kChunkBytes, &tmA, bar, m0 + 64 * c, k0, pol);
                         }
                     }
                     for (int b = 0; b < nbox; ++b) {
                         if (OP == kWgrad)
-                            tma_load_2d(sB + b * kChunkBytes, &tmB, &full[stage], t.row0 + 64 * b, k0, pol);
+                            tma_load_2d_pair(sB + b * kChunkBytes, &tmB, bar, row0 + 64 * b, k0, pol);
                         else
-                            tma_load_2d(sB + b * box_bytes, &tmB, &full[stage], k0, t.row0 + b * args.box_rows, pol);
+                            tma_load_2d_pair(sB + b * box_bytes, &tmB, bar, k0, row0 + b * args.box_rows, pol);
                     }
                     if (++stage == kStages) { stage = 0; phase ^= 1; }
                 }
             }
+            // Nothing may be in flight towards this CTA when it ends: on success
+            // every stage has been consumed (the leader's arrivals on `empty`
+            // included), otherwise every armed stage must have landed (the
+            // leader's barriers count for both; the pair ends together).
+            volatile int never = 0;
+            for (int s = 0; s < kStages && ok; ++s) {
+                ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
+                if (++stage == kStages) { stage = 0; phase ^= 1; }
+            }
             if (!ok) {
                 *abort_flag = 1;
                 atomicOr(args.status, DEV_TIMEOUT);
+                for (int s = 0; s < kStages; ++s)
+                    if (armed[s] >= 0 && !mbar_wait(&full[s], (uint32_t)armed[s], &never))
+                        atomicOr(args.status, DEV_TIMEOUT);
             }
-            // drain: every armed stage must have landed before the CTA exits
-            volatile int never = 0;
-            for (int s = 0; s < kStages; ++s)
-                if (armed[s] >= 0 && !mbar_wait(&full[s], (uint32_t)armed[s], &never))
-                    atomicOr(args.status, DEV_TIMEOUT);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer ------
+        // ------------------------------------ MMA issuer / relay ------
         constexpr uint32_t kMajor = (OP == kFwd ? 0u : 1u << 15) | (OP == kWgrad ? 1u << 16 : 0u);
         constexpr int kStepA = OP == kFwd ? 2 : 128, kStepB = OP == kWgrad ? 128 : 2;   // 16-byte units per 16 k
         int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        uint32_t phase = 0, acc_phase = 0, ragged_turn = 0;
+        const bool issuer = elect_one();
         bool ok = true;
-        for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
+        for (int w = pair; w < total && ok; w += pairs) {
             const MmTile t = mm_tile<OP>(w, args, s_beg, s_end, s_tiles, MT, NT);
             if (t.nrows == 0 || t.red == 0) continue;
             const int KB = (t.red + kBK - 1) / kBK;
-            const uint32_t idesc = idesc_bf16(kBM, (t.nrows + 15) & ~15) | kMajor;
-            if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag)) { ok = false; break; }
+            const int bn = (t.nrows + 15) & ~15;
+            const uint32_t idesc = idesc_bf16(kTM, bn) | kMajor;
+            if (rank == 0 && !mbar_wait_cluster(&tempty[acc], acc_phase ^ 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const uint32_t d = tmem_base + acc * kBN;
             for (int kb = 0; kb < KB; ++kb) {
-                if (!mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
                 uint8_t *sA = ring + stage * kStageBytes;
                 const int left = t.red - kb * kBK;
                 const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
-                if (OP == kWgrad && left < kBK && (left & 15)) {
+                const bool ragged = ragged_end<OP>(t, kb);
+                const uint32_t turn = (ragged_turn >> stage) & 1u;      // phase of this stage's ragged ends
+                if (rank == 0 || ragged) {
+                    if (!mbar_wait(&full[stage], rank == 0 ? phase : turn, abort_flag)) { ok = false; break; }
+                }
+                if (ragged) {
                     // rows [left, steps*16) belong to the next expert: zero
                     // them in every 64-column chunk of both operands
                     const int z = steps * 16 - left;
-                    const int chunks = kBM / 64 + (t.nrows + 63) / 64;
+                    const int chunks = kBM / 64 + (bn / 2 + 63) / 64;
                     for (int i = lane; i < chunks * z * 8; i += 32) {
                         const int c = i / (z * 8), b = i - c * z * 8;
                         *reinterpret_cast<uint4 *>(sA + c * kChunkBytes + left * 128 + b * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
+                    ragged_turn ^= 1u << stage;
+                    if (rank != 0) {
+                        if (lane == 0) mbar_arrive_leader_release(&relay[stage]);
+                    } else if (!mbar_wait_cluster(&relay[stage], turn, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
                 }
-                if (lane == 0) {
+                if (rank != 0) {
+                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    continue;
+                }
+                if (issuer) {
                     tc_fence_after();
                     const uint32_t sa = smem_u32(sA);
                     const uint64_t da = OP == kFwd ? sdesc_sw128(sa) : sdesc_mn(sa);
                     const uint64_t db = OP == kWgrad ? sdesc_mn(sa + kABytes) : sdesc_sw128(sa + kABytes);
-                    for (int k = 0; k < steps; ++k)
-                        mma_bf16_ss(d, da + kStepA * k, db + kStepB * k, idesc, (kb | k) != 0);
-                    mma_commit(&empty[stage]);
+                    if (steps == kBK / 16) {
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k)
+                            mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (kb | k) != 0);
+                    } else {
+                        for (int k = 0; k < steps; ++k)
+                            mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (kb | k) != 0);
+                    }
+                    mma_commit_pair(&empty[stage]);
                 }
                 __syncwarp();
                 if (++stage == kStages) { stage = 0; phase ^= 1; }
             }
             if (!ok) break;
-            if (lane == 0) mma_commit(&tfull[acc]);
+            if (rank == 0 && issuer) mma_commit_pair(&tfull[acc]);
             __syncwarp();
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
-        if (lane == 0) {
+        if (issuer) {
             if (!ok) {
                 *abort_flag = 1;
                 atomicOr(args.status, DEV_TIMEOUT);
             }
-            // no MMA may be reading this CTA's shared memory when it exits
-            volatile int never = 0;
-            mma_commit(drained);
-            if (!mbar_wait(drained, 0, &never)) atomicOr(args.status, DEV_TIMEOUT);
+            // no MMA may be reading either CTA's shared memory when they end
+            if (rank == 0) {
+                volatile int never = 0;
+                mma_commit_leader(drained);
+                if (!mbar_wait(drained, 0, &never)) atomicOr(args.status, DEV_TIMEOUT);
+            }
         }
         __syncwarp();
     } else {
@@ -314,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __nv_bfloat16 *stg = s_out + ew * 32 * 32;   // [32 rows][32 columns]
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int w = blockIdx.x; w < total; w += gridDim.x) {
+        for (int w = pair; w < total; w += pairs) {
             const MmTile t = mm_tile<OP>(w, args, s_beg, s_end, s_tiles, MT, NT);
             if (t.nrows == 0) continue;
             const bool none = OP == kWgrad && t.red == 0;     // an expert without rows: the sum is zero
@@ -329,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t tb = tmem_base + ((uint32_t)(eg * 32) << 16) + acc * kBN;
             const size_t orow = OP == kWgrad ? (size_t)t.e * args.N + t.row0 : (size_t)t.row0;
-            const int mw = t.m0 + eg * 32;      // first output column of this warp
+            const int mw = t.m0 + rank * kBM + eg * 32;      // first output column of this warp
             for (int c0 = half * 32; c0 < t.nrows; c0 += 64) {
                 uint32_t g[32];
                 if (none) {
@@ -357,27 +514,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 } else if (mw + lane < args.M) {
                     const size_t at = (orow + c0) * args.M + mw + lane;
+                    if (OP == kWgrad && args.base) {     // all reads first: base may be out itself
+                        float b[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (c0 + j < t.nrows) {
-                            float v = __uint_as_float(g[j]);
-                            if (OP == kWgrad && args.base) v += args.base[at + (size_t)j * args.M];
-                            static_cast<float *>(args.out)[at + (size_t)j * args.M] = v;
-                        }
+                        for (int j = 0; j < 32; ++j) b[j] = c0 + j < t.nrows ? args.base[at + (size_t)j * args.M] : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(__uint_as_float(g[j]) + b[j]);
                     }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < t.nrows) static_cast<float *>(args.out)[at + (size_t)j * args.M] = __uint_as_float(g[j]);
                 }
             }
             if (none) continue;
             tc_fence_before();
-            mbar_arrive(&tempty[acc]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_leader(&tempty[acc]);
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
     }
     tc_fence_before();
     __syncthreads();
+    __syncwarp();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, 512);
+        tmem_dealloc_pair(tmem_base, 512);
     }
 }
 
@@ -400,7 +562,7 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const MmArgs &arg
     static std::atomic<int> attr_done[64];
     const cudaError_t e = enable_max_dyn_smem((const void *)grouped_mm<OP, OUT_BF16>, attr_done);
     if (e != cudaSuccess) return e;
-    return launch_k(grouped_mm<OP, OUT_BF16>, dim3(num_sms()), dim3(kThreads), smem_bytes(args.E), st, true, a, b, args);
+    return launch_k(grouped_mm<OP, OUT_BF16>, dim3(num_sms() & ~1), dim3(kThreads), smem_bytes(args.E), st, true, a, b, args);
 }
 
 }  // namespace
