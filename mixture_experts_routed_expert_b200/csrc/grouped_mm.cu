@@ -22,14 +22,16 @@
 // gradient: the rows behind it in the last 16-row step are overwritten with
 // zeros in shared memory, on both operands, before the MMA reads them (a
 // zero on one side alone would let a neighbour's infinity through as NaN).
+// TMA writes those zeros too, as boxes that lie wholly outside the matrix:
+// stores by the CTA's threads would need a release to the other CTA, whose
+// fence (about 2000 cycles a tile) cost 13 us of 95 at 64 experts x 192 rows.
 //
 // Persistent: one CTA per SM, the pairs walk the tile list, which every CTA
 // derives from the offsets on the device.  Warp roles: 0 TMA producer of the
 // CTA's own operands (both CTAs' copies complete on the leading CTA's
-// barrier); 1 in the leading CTA MMA issue for the pair, in the other idle
-// but for a ragged end, which each CTA zeroes in its own operands before the
-// other CTA's warp tells the leader; 2-9 epilogue (two warps per TMEM lane
-// quarter, alternating 32 columns).
+// barrier); 1 in the leading CTA MMA issue for the pair; 2-9 epilogue (two
+// sets of four warps, one warp per TMEM lane quarter, alternating 32
+// accumulator columns); 10 (weight gradient) zeroes the ragged end.
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -44,18 +46,23 @@ enum Op : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
 constexpr int kBK = 64;                        // reduction elements per stage = one 128-byte swizzle row
 constexpr int kTM = 256;                       // A-side width of a pair's tile
-constexpr int kBN = 256;                       // B-side width of a pair's tile
-constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kABytes = kBM * 128;
-constexpr int kBBytes = kBN / 2 * 128;         // a CTA holds half of B
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kRingBytes = kStages * kStageBytes;
-constexpr int kOutStage = kEpiWarps * 32 * 32 * 2;
+constexpr int kOutStage = 2 * 32 * kBM * 2;    // per epilogue set 32 rows x 128 columns of bf16
 constexpr int kChunkBytes = 64 * 128;          // MN-major: 64 elements x 64 reduction rows
+constexpr int kRaggedDelay = 3;                // k-blocks multiplied before a ragged one that was loaded first
 
-size_t smem_bytes(int E) { return 1024 + kRingBytes + 1024 + kOutStage + align_up(12 * (size_t)(E + 1), 16); }
+// BN: B-side width of a pair's tile; each CTA holds half of B.
+template <int OP, int BN>
+struct MmCfg {
+    static constexpr int kStages = BN == 256 ? 6 : 9;
+    static constexpr int kBBytes = BN / 2 * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kThreads = 64 + 32 * kEpiWarps + (OP == kWgrad ? 32 : 0);
+    static_assert(kRaggedDelay + 2 <= kStages && (OP != kWgrad || BN / 2 % 64 == 0), "");
+    static size_t smem_bytes(int E) { return 1024 + kRingBytes + 1024 + kOutStage + align_up(12 * (size_t)(E + 1), 16); }
+};
 
 struct MmArgs {
     const int32_t *offsets;   // [E+1]
@@ -66,6 +73,12 @@ struct MmArgs {
     void *out;
     const float *base;        // weight gradient: added to the product (may be out itself), or null
     int32_t *status;
+};
+
+// 64 columns x 4 and x 1 rows of the row matrix: boxes behind its last row
+// are filled with zeros (weight gradient).
+struct ZeroMaps {
+    CUtensorMap rows4, rows1;
 };
 
 // One tile: expert, first A-side column, first B-side row (of the row matrix,
@@ -98,6 +111,43 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// 16 TMEM lanes x 32 columns: register 4i + 2o + c of a thread holds lane
+// 8o + lane/4, column 8i + 2(lane%4) + c.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Four transposed 8x8 b16 matrices: lane 8q + j gives the address of row j of matrix q.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, const uint32_t (&p)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(p[0]),
+                 "r"(p[1]), "r"(p[2]), "r"(p[3])
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t saddr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// named_barrier that also says whether every thread brought a true `v`.
+__device__ __forceinline__ bool named_barrier_all(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
 // True in one lane of a converged warp (the same on every call).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -110,14 +160,9 @@ __device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
     return a;
 }
-// Arrive on the leading CTA's barrier; the cluster-scope release (about 2000
-// cycles: every block of a product taking it ran at half the speed) is for
-// shared-memory writes of this thread that the leader's MMAs read.
+// Arrive on the leading CTA's barrier.
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_leader_release(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
 }
 // TMA tile loads into this CTA's shared memory that complete on a barrier of
 // either CTA of the pair (no multicast).
@@ -136,27 +181,6 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         "cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
         : "memory");
-}
-// mbar_wait for arrivals from the other CTA (cluster scope).
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    const uint32_t a = smem_u32(bar);
-    long long t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(a), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (it == 0) t0 = clock64();
-        if ((it & 255u) == 255u) {
-            if (*abort) return false;
-            if (clock64() - t0 > kWaitLimitCycles) return false;
-        }
-    }
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
@@ -191,7 +215,7 @@ __device__ __forceinline__ void mma_commit_leader(uint64_t *bar) {
                  : "memory");
 }
 
-template <int OP>
+template <int OP, int BN>
 __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t *s_beg, const int32_t *s_end,
                                           const int32_t *s_tiles, int MT, int NT) {
     MmTile t;
@@ -200,8 +224,8 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
         const int local = w - t.e * MT * NT;
         const int n = local / MT;
         t.m0 = (local - n * MT) * kTM;
-        t.row0 = n * kBN;
-        t.nrows = min(kBN, a.N - t.row0);
+        t.row0 = n * BN;
+        t.nrows = min(BN, a.N - t.row0);
         t.red0 = s_beg[t.e];
         t.red = s_end[t.e] - t.red0;
     } else {
@@ -215,7 +239,7 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
         const int local = w - s_tiles[lo] * MT;
         const int m = local / nt, n = local - m * nt;
         const int n_e = s_end[lo] - s_beg[lo];
-        const int rpt = min(kBN, ((n_e + nt - 1) / nt + 15) & ~15);
+        const int rpt = min(BN, ((n_e + nt - 1) / nt + 15) & ~15);
         t.m0 = m * kTM;
         t.row0 = s_beg[lo] + n * rpt;
         t.nrows = max(0, min(rpt, n_e - n * rpt));
@@ -225,32 +249,33 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
     return t;
 }
 
-// Whether k-block kb ends inside a 16-row step with the next expert's rows in it.
+// Whether the reduction ends inside a 16-row step, with the next expert's rows behind it.
 template <int OP>
-__device__ __forceinline__ bool ragged_end(const MmTile &t, int kb) {
-    const int left = t.red - kb * kBK;
-    return OP == kWgrad && left < kBK && (left & 15);
+__device__ __forceinline__ bool ragged_end(const MmTile &t) {
+    return OP == kWgrad && (t.red & 15);
 }
 
-template <int OP, bool OUT_BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    grouped_mm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const MmArgs args) {
+template <int OP, bool OUT_BF16, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThreads), 1)
+    grouped_mm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ ZeroMaps zero, const MmArgs args) {
+    using C = MmCfg<OP, BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem;
-    // full: the leader's counts both CTAs' copies, but for a ragged end, where
-    // each CTA's own barrier counts its own and `relay` follows
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRingBytes);
-    uint64_t *empty = full + kStages;
-    uint64_t *tfull = empty + kStages;
+    // full: the leader's counts both CTAs' copies.  A ragged end lands on
+    // rfull, each CTA's own, and then its zeros on the leader's full.
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kRingBytes);
+    uint64_t *empty = full + C::kStages;
+    uint64_t *tfull = empty + C::kStages;
     uint64_t *tempty = tfull + 2;              // the leader's, for both CTAs' epilogues
-    uint64_t *relay = tempty + 2;              // the leader's: the other CTA's ragged end is zeroed
-    uint64_t *drained = relay + kStages;
+    uint64_t *rfull = tempty + 2;
+    uint64_t *drained = rfull + C::kStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int32_t *s_part = reinterpret_cast<int32_t *>(tmem_slot + 2);          // [kThreads / 32]
-    __nv_bfloat16 *s_out = reinterpret_cast<__nv_bfloat16 *>(smem + kRingBytes + 1024);
-    int32_t *s_beg = reinterpret_cast<int32_t *>(smem + kRingBytes + 1024 + kOutStage);
+    int32_t *s_part = reinterpret_cast<int32_t *>(tmem_slot + 2);          // [C::kThreads / 32]
+    uint8_t *s_out = smem + C::kRingBytes + 1024;
+    int32_t *s_beg = reinterpret_cast<int32_t *>(smem + C::kRingBytes + 1024 + kOutStage);
     int32_t *s_end = s_beg + args.E;
     int32_t *s_tiles = s_end + args.E;                                      // [E+1]
 
@@ -258,10 +283,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rank = (int)cluster_rank();      // 0: the leader
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&relay[s], 1);
+            mbar_init(&rfull[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
@@ -278,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Row ranges of the experts, clamped into the matrices whatever the
     // offsets hold, and the prefix sum of their row tiles: each thread sums a
     // run of experts, then warps and block are scanned.
-    const int per = (args.E + kThreads - 1) / kThreads;
+    const int per = (args.E + C::kThreads - 1) / C::kThreads;
     const int e0 = min(args.E, (int)threadIdx.x * per), e1 = min(args.E, e0 + per);
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
@@ -286,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n = min(max(__ldg(args.offsets + e + 1), b), args.rows);
         s_beg[e] = b;
         s_end[e] = n;
-        sum += (n - b + kBN - 1) / kBN;
+        sum += (n - b + BN - 1) / BN;
     }
     int incl = sum;
 #pragma unroll
@@ -300,9 +325,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < warp; ++i) before += s_part[i];
     for (int e = e0; e < e1; ++e) {
         s_tiles[e] = before;
-        before += (s_end[e] - s_beg[e] + kBN - 1) / kBN;
+        before += (s_end[e] - s_beg[e] + BN - 1) / BN;
     }
-    if (threadIdx.x == kThreads - 1) s_tiles[args.E] = before;
+    if (threadIdx.x == C::kThreads - 1) s_tiles[args.E] = before;
     tc_fence_before();
     __syncthreads();
     __syncwarp();
@@ -310,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int MT = (args.M + kTM - 1) / kTM;
-    const int NT = (args.N + kBN - 1) / kBN;
+    const int NT = (args.N + BN - 1) / BN;
     const int total = OP == kWgrad ? args.E * MT * NT : s_tiles[args.E] * MT;
     pdl_launch_dependents();
 
@@ -320,12 +345,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t pol = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0;
-            int armed[kStages];
-#pragma unroll
-            for (int s = 0; s < kStages; ++s) armed[s] = -1;
+            uint32_t used = 0, last = 0, rused = 0, rturn = 0;   // per stage: full in use yet, its last parity; rfull likewise
             bool ok = true;
             for (int w = pair; w < total && ok; w += pairs) {
-                const MmTile t = mm_tile<OP>(w, args, s_beg, s_end, s_tiles, MT, NT);
+                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
                 if (t.nrows == 0) continue;
                 const int KB = (t.red + kBK - 1) / kBK;
                 const int half = ((t.nrows + 15) & ~15) / 2;         // B rows of each CTA
@@ -333,14 +356,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int nbox = OP == kWgrad ? (half + 63) / 64 : (half + args.box_rows - 1) / args.box_rows;
                 const int box_bytes = OP == kWgrad ? kChunkBytes : args.box_rows * 128;
                 const uint32_t bytes = kABytes + nbox * box_bytes;
-                for (int kb = 0; kb < KB; ++kb) {
+                const bool ends_ragged = ragged_end<OP>(t);
+                for (int i = 0; i < KB; ++i) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-                    uint8_t *sA = ring + stage * kStageBytes;
+                    uint8_t *sA = ring + stage * C::kStageBytes;
                     uint8_t *sB = sA + kABytes;
-                    const bool ragged = ragged_end<OP>(t, kb);
-                    if (rank == 0 || ragged) mbar_arrive_expect_tx(&full[stage], ragged ? bytes : 2 * bytes);
-                    if (rank == 0) armed[stage] = (int)phase;
-                    const uint32_t bar = ragged ? smem_u32(&full[stage]) : leader_addr(&full[stage]);
+                    const bool ragged = ends_ragged && i == 0;          // the ragged end is loaded first
+                    const int kb = ends_ragged ? (i == 0 ? KB - 1 : i - 1) : i;
+                    if (ragged) {
+                        mbar_arrive_expect_tx(&rfull[stage], bytes);
+                        rused |= 1u << stage;
+                        rturn ^= 1u << stage;
+                    } else if (rank == 0) {
+                        mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+                    }
+                    if (rank == 0) {
+                        used |= 1u << stage;
+                        last = (last & ~(1u << stage)) | (phase << stage);
+                    }
+                    const uint32_t bar = ragged ? smem_u32(&rfull[stage]) : leader_addr(&full[stage]);
                     const int k0 = t.red0 + kb * kBK;
                     if (OP == kFwd) {
                         tma_load_3d_pair(sA, &tmA, bar, k0, m0, t.e, pol);
@@ -358,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         else
                             tma_load_2d_pair(sB + b * box_bytes, &tmB, bar, k0, row0 + b * args.box_rows, pol);
                     }
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1; }
                 }
             }
             // Nothing may be in flight towards this CTA when it ends: on success
@@ -366,172 +400,236 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // included), otherwise every armed stage must have landed (the
             // leader's barriers count for both; the pair ends together).
             volatile int never = 0;
-            for (int s = 0; s < kStages && ok; ++s) {
+            for (int s = 0; s < C::kStages && ok; ++s) {
                 ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag);
-                if (++stage == kStages) { stage = 0; phase ^= 1; }
+                if (++stage == C::kStages) { stage = 0; phase ^= 1; }
             }
             if (!ok) {
                 *abort_flag = 1;
                 atomicOr(args.status, DEV_TIMEOUT);
-                for (int s = 0; s < kStages; ++s)
-                    if (armed[s] >= 0 && !mbar_wait(&full[s], (uint32_t)armed[s], &never))
-                        atomicOr(args.status, DEV_TIMEOUT);
+                for (int s = 0; s < C::kStages; ++s) {
+                    if ((used >> s) & 1u) mbar_wait(&full[s], (last >> s) & 1u, &never);
+                    if ((rused >> s) & 1u) mbar_wait(&rfull[s], (rturn >> s & 1u) ^ 1u, &never);
+                }
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------ MMA issuer / relay ------
-        constexpr uint32_t kMajor = (OP == kFwd ? 0u : 1u << 15) | (OP == kWgrad ? 1u << 16 : 0u);
-        constexpr int kStepA = OP == kFwd ? 2 : 128, kStepB = OP == kWgrad ? 128 : 2;   // 16-byte units per 16 k
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0, ragged_turn = 0;
-        const bool issuer = elect_one();
-        bool ok = true;
-        for (int w = pair; w < total && ok; w += pairs) {
-            const MmTile t = mm_tile<OP>(w, args, s_beg, s_end, s_tiles, MT, NT);
-            if (t.nrows == 0 || t.red == 0) continue;
-            const int KB = (t.red + kBK - 1) / kBK;
-            const int bn = (t.nrows + 15) & ~15;
-            const uint32_t idesc = idesc_bf16(kTM, bn) | kMajor;
-            if (rank == 0 && !mbar_wait_cluster(&tempty[acc], acc_phase ^ 1, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t d = tmem_base + acc * kBN;
-            for (int kb = 0; kb < KB; ++kb) {
-                uint8_t *sA = ring + stage * kStageBytes;
-                const int left = t.red - kb * kBK;
-                const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
-                const bool ragged = ragged_end<OP>(t, kb);
-                const uint32_t turn = (ragged_turn >> stage) & 1u;      // phase of this stage's ragged ends
-                if (rank == 0 || ragged) {
-                    if (!mbar_wait(&full[stage], rank == 0 ? phase : turn, abort_flag)) { ok = false; break; }
-                }
-                if (ragged) {
-                    // rows [left, steps*16) belong to the next expert: zero
-                    // them in every 64-column chunk of both operands
-                    const int z = steps * 16 - left;
-                    const int chunks = kBM / 64 + (bn / 2 + 63) / 64;
-                    for (int i = lane; i < chunks * z * 8; i += 32) {
-                        const int c = i / (z * 8), b = i - c * z * 8;
-                        *reinterpret_cast<uint4 *>(sA + c * kChunkBytes + left * 128 + b * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    ragged_turn ^= 1u << stage;
-                    if (rank != 0) {
-                        if (lane == 0) mbar_arrive_leader_release(&relay[stage]);
-                    } else if (!mbar_wait_cluster(&relay[stage], turn, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (rank != 0) {
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
-                    continue;
-                }
-                if (issuer) {
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(sA);
-                    const uint64_t da = OP == kFwd ? sdesc_sw128(sa) : sdesc_mn(sa);
-                    const uint64_t db = OP == kWgrad ? sdesc_mn(sa + kABytes) : sdesc_sw128(sa + kABytes);
-                    if (steps == kBK / 16) {
+        // ------------------------------------------------ MMA issuer ------
+        if (rank == 0) {
+            constexpr uint32_t kMajor = (OP == kFwd ? 0u : 1u << 15) | (OP == kWgrad ? 1u << 16 : 0u);
+            constexpr int kStepA = OP == kFwd ? 2 : 128, kStepB = OP == kWgrad ? 128 : 2;   // 16-byte units per 16 k
+            int stage0 = 0, acc = 0;            // ring place of the tile's first k-block, and its phase
+            uint32_t phase0 = 0, acc_phase = 0;
+            const bool issuer = elect_one();
+            bool ok = true;
+            for (int w = pair; w < total && ok; w += pairs) {
+                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
+                if (t.nrows == 0 || t.red == 0) continue;
+                const int KB = (t.red + kBK - 1) / kBK;
+                const uint32_t idesc = idesc_bf16(kTM, (t.nrows + 15) & ~15) | kMajor;
+                if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem_base + acc * BN;
+                const bool ends_ragged = ragged_end<OP>(t);
+                const int delay = ends_ragged ? min(KB - 1, kRaggedDelay) : 0;
+                int stage = stage0;
+                uint32_t phase = phase0;
+                for (int i = 0; i < KB; ++i) {
+                    // the ragged k-block sits in the first stage; its turn comes after `delay` others
+                    const bool ragged = ends_ragged && i == delay;
+                    if (ends_ragged && i == 0 && !ragged && ++stage == C::kStages) { stage = 0; phase ^= 1; }
+                    const int at = ragged ? stage0 : stage;
+                    if (!mbar_wait(&full[at], ragged ? phase0 : phase, abort_flag)) { ok = false; break; }
+                    const int left = t.red - (ragged ? KB - 1 : ends_ragged ? i - (i > delay) : i) * kBK;
+                    const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
+                    if (issuer) {
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(ring + at * C::kStageBytes);
+                        const uint64_t da = OP == kFwd ? sdesc_sw128(sa) : sdesc_mn(sa);
+                        const uint64_t db = OP == kWgrad ? sdesc_mn(sa + kABytes) : sdesc_sw128(sa + kABytes);
+                        if (steps == kBK / 16) {
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k)
-                            mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (kb | k) != 0);
-                    } else {
-                        for (int k = 0; k < steps; ++k)
-                            mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (kb | k) != 0);
+                            for (int k = 0; k < kBK / 16; ++k)
+                                mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (i | k) != 0);
+                        } else {
+                            for (int k = 0; k < steps; ++k)
+                                mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (i | k) != 0);
+                        }
+                        mma_commit_pair(&empty[at]);
                     }
-                    mma_commit_pair(&empty[stage]);
+                    __syncwarp();
+                    if ((!ragged || KB == 1) && ++stage == C::kStages) { stage = 0; phase ^= 1; }
                 }
+                if (!ok) break;
+                stage0 = stage;
+                phase0 = phase;
+                if (issuer) mma_commit_pair(&tfull[acc]);
                 __syncwarp();
-                if (++stage == kStages) { stage = 0; phase ^= 1; }
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             }
-            if (!ok) break;
-            if (rank == 0 && issuer) mma_commit_pair(&tfull[acc]);
-            __syncwarp();
-            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
-        }
-        if (issuer) {
-            if (!ok) {
-                *abort_flag = 1;
-                atomicOr(args.status, DEV_TIMEOUT);
-            }
-            // no MMA may be reading either CTA's shared memory when they end
-            if (rank == 0) {
+            if (issuer) {
+                if (!ok) {
+                    *abort_flag = 1;
+                    atomicOr(args.status, DEV_TIMEOUT);
+                }
+                // no MMA may be reading either CTA's shared memory when they end
                 volatile int never = 0;
                 mma_commit_leader(drained);
                 if (!mbar_wait(drained, 0, &never)) atomicOr(args.status, DEV_TIMEOUT);
+            }
+            __syncwarp();
+        }
+    } else if (OP == kWgrad && warp == 2 + kEpiWarps) {
+        // ------------------------------------------------ ragged ends -----
+        // In the last k-block of an expert the rows from `left` up to the end
+        // of their 16-row step belong to the next expert: once the block has
+        // landed, zero them in every 64-column chunk of this CTA's operands.
+        // The block is loaded before the tile's others and multiplied after up
+        // to kRaggedDelay of them, which hides the second trip.
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_last();
+            int stage = 0;
+            uint32_t turn = 0;
+            for (int w = pair; w < total; w += pairs) {
+                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
+                if (t.nrows == 0 || t.red == 0) continue;
+                const int KB = (t.red + kBK - 1) / kBK;
+                if (ragged_end<OP>(t)) {
+                    if (!mbar_wait(&rfull[stage], (turn >> stage) & 1u, abort_flag)) {
+                        *abort_flag = 1;
+                        atomicOr(args.status, DEV_TIMEOUT);
+                        break;
+                    }
+                    turn ^= 1u << stage;
+                    const int left = t.red - (KB - 1) * kBK;
+                    const int z = ((left + 15) & ~15) - left;
+                    const int chunks = kBM / 64 + (((t.nrows + 15) & ~15) / 2 + 63) / 64;
+                    const uint32_t bar = leader_addr(&full[stage]);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * chunks * z * 128);
+                    for (int c = 0; c < chunks; ++c) {
+                        uint8_t *p = ring + stage * C::kStageBytes + c * kChunkBytes + left * 128;
+                        int r = 0;
+                        for (; r + 4 <= z; r += 4) tma_load_2d_pair(p + r * 128, &zero.rows4, bar, 0, args.rows, pol);
+                        for (; r < z; ++r) tma_load_2d_pair(p + r * 128, &zero.rows1, bar, 0, args.rows, pol);
+                    }
+                }
+                stage = (stage + KB) % C::kStages;
             }
         }
         __syncwarp();
     } else {
         // ------------------------------------------------ epilogue --------
-        const int ew = warp - 2;                // 0 .. kEpiWarps-1
         const int eg = warp & 3;                // TMEM lanes [32*eg, 32*eg+32)
-        const int half = ew >> 2;               // which 32-column chunks
-        __nv_bfloat16 *stg = s_out + ew * 32 * 32;   // [32 rows][32 columns]
+        const int set = (warp - 2) >> 2;        // which 32-column chunks
+        const uint32_t stg = smem_u32(s_out) + set * (32 * kBM * 2);   // [32 rows][16 units of 8 columns]
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int w = pair; w < total; w += pairs) {
-            const MmTile t = mm_tile<OP>(w, args, s_beg, s_end, s_tiles, MT, NT);
+            const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
             if (t.nrows == 0) continue;
             const bool none = OP == kWgrad && t.red == 0;     // an expert without rows: the sum is zero
             if (none && args.base == args.out && args.base != nullptr) continue;
+            const size_t orow = OP == kWgrad ? (size_t)t.e * args.N + t.row0 : (size_t)t.row0;
+            const int mc = t.m0 + rank * kBM;   // first output column of this CTA
+            // fp32: first output element of this lane in a chunk, and the base of
+            // the chunk to come (read a chunk ahead of its use, before any store
+            // of the chunk: base may be out itself)
+            const bool mine = mc + eg * 32 + lane < args.M;
+            const size_t at0 = orow * args.M + mc + eg * 32 + lane;
+            float b[32];
+            auto read_base = [&](int c0) {
+                if (OP != kWgrad || OUT_BF16 || args.base == nullptr || !mine) return;
+                const float *p = args.base + at0 + (size_t)c0 * args.M;
+                if (c0 + 32 <= t.nrows) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = __ldcs(p);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = c0 + j < t.nrows ? __ldcs(p) : 0.f;
+                }
+            };
+            read_base(set * 32);
             if (!none) {
-                if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) {
+                // the set's warps agree, so that none waits for another below
+                if (!named_barrier_all(1 + set, 128, mbar_wait(&tfull[acc], acc_phase, abort_flag))) {
                     *abort_flag = 1;
                     atomicOr(args.status, DEV_TIMEOUT);
                     break;
                 }
                 tc_fence_after();
             }
-            const uint32_t tb = tmem_base + ((uint32_t)(eg * 32) << 16) + acc * kBN;
-            const size_t orow = OP == kWgrad ? (size_t)t.e * args.N + t.row0 : (size_t)t.row0;
-            const int mw = t.m0 + rank * kBM + eg * 32;      // first output column of this warp
-            for (int c0 = half * 32; c0 < t.nrows; c0 += 64) {
+            const uint32_t tb = tmem_base + ((uint32_t)(eg * 32) << 16) + acc * BN;
+            // the accumulator is free again once this warp's last chunk is in registers
+            auto release = [&]() {
+                if (none) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_leader(&tempty[acc]);
+            };
+            if (set * 32 >= t.nrows) release();
+            for (int c0 = set * 32; c0 < t.nrows; c0 += 64) {
                 uint32_t g[32];
                 if (none) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) g[j] = 0;
+                } else if (OUT_BF16) {
+                    tmem_ld_16x32(tb + c0, g);
+                    tmem_ld_16x32(tb + c0 + (16u << 16), g + 16);
+                    tmem_ld_wait();
                 } else {
                     tmem_ld32(tb + c0, g);
                     tmem_ld_wait();
                 }
+                if (c0 + 64 >= t.nrows) release();
                 if (OUT_BF16) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) stg[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(g[j]));
-                    __syncwarp();
-                    // 32 rows x 64 bytes: four lanes per row, 16 bytes each
-                    const int q = lane & 3;
+                    // g[h*16 + i*4 + o*2 + {0,1}]: TMEM lane h*16 + o*8 + lane/4, columns 8i + 2(lane%4) + {0,1}.
+                    // Transposed 8x8 blocks to shared memory: row = accumulator column, 16-byte
+                    // units of 8 lanes, unit index xor row % 8 (no bank conflicts either way).
+                    const int q = lane >> 3, jj = lane & 7;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = (lane >> 2) + 8 * i;
-                        if (c0 + r < t.nrows && mw + q * 8 < args.M) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 32 + q * 8);
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(args.out) +
-                                                       (orow + c0 + r) * args.M + mw + q * 8) = v;
-                        }
-                    }
-                    __syncwarp();
-                } else if (mw + lane < args.M) {
-                    const size_t at = (orow + c0) * args.M + mw + lane;
-                    if (OP == kWgrad && args.base) {     // all reads first: base may be out itself
-                        float b[32];
+                        uint32_t p[4];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) b[j] = c0 + j < t.nrows ? args.base[at + (size_t)j * args.M] : 0.f;
+                        for (int o = 0; o < 4; ++o) {
+                            const uint32_t *v = g + (o >> 1) * 16 + i * 4 + (o & 1) * 2;
+                            p[o] = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                        }
+                        stmatrix4_trans(stg + (8 * i + jj) * (kBM * 2) + (((eg * 4 + q) ^ jj) << 4), p);
+                    }
+                    named_barrier(1 + set, 128);
+                    // 8 rows per warp, 256 contiguous bytes each
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = eg * 8 + i * 2 + (lane >> 4), u = lane & 15;
+                        const uint4 v = ld_shared16(stg + r * (kBM * 2) + ((u ^ (r & 7)) << 4));
+                        if (c0 + r < t.nrows && mc + u * 8 < args.M)
+                            __stcs(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(args.out) +
+                                                             (orow + c0 + r) * args.M + mc + u * 8), v);
+                    }
+                    named_barrier(1 + set, 128);
+                } else {
+                    if (OP == kWgrad && args.base) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(__uint_as_float(g[j]) + b[j]);
+                        read_base(c0 + 64);
                     }
+                    // one check a chunk: a compare, a branch and a 64-bit product a store
+                    // made 600 instructions of a chunk and held the stores at 3 TB/s
+                    float *o = static_cast<float *>(args.out) + at0 + (size_t)c0 * args.M;
+                    if (mine && c0 + 32 <= t.nrows) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c0 + j < t.nrows) static_cast<float *>(args.out)[at + (size_t)j * args.M] = __uint_as_float(g[j]);
+                        for (int j = 0; j < 32; ++j, o += args.M) __stcs(o, __uint_as_float(g[j]));
+                    } else if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, o += args.M)
+                            if (c0 + j < t.nrows) __stcs(o, __uint_as_float(g[j]));
+                    }
                 }
             }
             if (none) continue;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_leader(&tempty[acc]);
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -557,12 +655,35 @@ bool make_tmap_3d(CUtensorMap *m, const void *ptr, uint64_t depth, uint64_t rows
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int OP, bool OUT_BF16>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const MmArgs &args, cudaStream_t st) {
+// Row-major [rows][cols] bf16 with boxes of box_rows x 64 columns, not
+// swizzled (they may start at any 128-byte row of a swizzled tile): for the
+// zeros behind its last row.
+bool make_tmap_zero(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+    auto enc = tmap_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int OP, bool OUT_BF16, int BN>
+cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const ZeroMaps &z, const MmArgs &args, cudaStream_t st) {
+    using C = MmCfg<OP, BN>;
     static std::atomic<int> attr_done[64];
-    const cudaError_t e = enable_max_dyn_smem((const void *)grouped_mm<OP, OUT_BF16>, attr_done);
+    const cudaError_t e = enable_max_dyn_smem((const void *)grouped_mm<OP, OUT_BF16, BN>, attr_done);
     if (e != cudaSuccess) return e;
-    return launch_k(grouped_mm<OP, OUT_BF16>, dim3(num_sms() & ~1), dim3(kThreads), smem_bytes(args.E), st, true, a, b, args);
+    return launch_k(grouped_mm<OP, OUT_BF16, BN>, dim3(num_sms() & ~1), dim3(C::kThreads), C::smem_bytes(args.E), st,
+                    true, a, b, z, args);
+}
+
+template <int OP, int BN>
+cudaError_t launch(bool out_bf16, const CUtensorMap &a, const CUtensorMap &b, const ZeroMaps &z, const MmArgs &args,
+                   cudaStream_t st) {
+    return out_bf16 ? launch<OP, true, BN>(a, b, z, args, st) : launch<OP, false, BN>(a, b, z, args, st);
 }
 
 }  // namespace
@@ -575,18 +696,19 @@ cudaError_t launch_grouped_mm(const void *x, const void *w, const int32_t *offse
     a.rows = rows;
     a.E = E;
     a.M = transpose ? C : N;
-    a.N = kBN;
     a.red = red;
-    a.box_rows = rows >= (int64_t)64 * E ? 128 : 32;
+    const bool few = rows <= (int64_t)32 * E;
+    a.box_rows = few ? 32 : 128;
     a.out = out;
     a.status = status;
     CUtensorMap ta, tb;
     if (!make_tmap_3d(&ta, w, E, N, C, transpose ? kBK : kBM) ||
         !make_tmap(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, rows, red, a.box_rows))
         return cudaErrorInvalidValue;
+    const ZeroMaps z = {};   // not used by these two
     if (transpose)
-        return out_bf16 ? launch<kDgrad, true>(ta, tb, a, st) : launch<kDgrad, false>(ta, tb, a, st);
-    return out_bf16 ? launch<kFwd, true>(ta, tb, a, st) : launch<kFwd, false>(ta, tb, a, st);
+        return few ? launch<kDgrad, 64>(out_bf16, ta, tb, z, a, st) : launch<kDgrad, 256>(out_bf16, ta, tb, z, a, st);
+    return few ? launch<kFwd, 64>(out_bf16, ta, tb, z, a, st) : launch<kFwd, 256>(out_bf16, ta, tb, z, a, st);
 }
 
 cudaError_t launch_grouped_wgrad(const void *dy, const void *x, const int32_t *offsets, int rows, int N, int C, int E,
@@ -601,10 +723,12 @@ cudaError_t launch_grouped_wgrad(const void *dy, const void *x, const int32_t *o
     a.base = base;
     a.status = status;
     CUtensorMap ta, tb;
+    ZeroMaps z;
     if (!make_tmap(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, rows, C, kBK) ||
-        !make_tmap(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, rows, N, kBK))
+        !make_tmap(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, rows, N, kBK) ||
+        !make_tmap_zero(&z.rows4, x, rows, C, 4) || !make_tmap_zero(&z.rows1, x, rows, C, 1))
         return cudaErrorInvalidValue;
-    return out_bf16 ? launch<kWgrad, true>(ta, tb, a, st) : launch<kWgrad, false>(ta, tb, a, st);
+    return launch<kWgrad, 256>(out_bf16, ta, tb, z, a, st);
 }
 
 }  // namespace moe

@@ -27,17 +27,17 @@ def mm64(x, offsets, w, transpose):
     """(result, sum of |products|) in 64 bits, zero rows where no expert owns them."""
     x, w = x.double(), w.double()
     rows, co = x.shape[0], w.shape[2 if transpose else 1]
-    y, s = torch.zeros(rows, co, dtype=torch.float64), torch.zeros(rows, co, dtype=torch.float64)
+    y, s = (torch.zeros(rows, co, dtype=torch.float64, device=x.device) for _ in range(2))
     for e, a, b in spans(offsets, rows):
         m = w[e] if transpose else w[e].t()
         y[a:b], s[a:b] = x[a:b] @ m, x[a:b].abs() @ m.abs()
     return y, s
 
 
-def wgrad64(dy, x, offsets, base=None):
+def wgrad64(dy, x, offsets, base=None, device=None):
     dy, x = dy.double(), x.double()
     E = len(offsets) - 1
-    y = torch.zeros(E, dy.shape[1], x.shape[1], dtype=torch.float64)
+    y = torch.zeros(E, dy.shape[1], x.shape[1], dtype=torch.float64, device=device)
     s = torch.zeros_like(y)
     for e, a, b in spans(offsets, x.shape[0]):
         y[e], s[e] = dy[a:b].t() @ x[a:b], dy[a:b].abs().t() @ x[a:b].abs()

@@ -149,6 +149,25 @@ def test_no_rows_at_all(moe, cuda_dev):
     assert torch.equal(moe.moe_grouped_mm_wgrad(dy, x, o, base=base), base)
 
 
+def test_several_tiles_per_cta_pair(moe, cuda_dev):
+    """Long ragged reductions, more tiles than SM pairs: the shared-memory ring
+    wraps inside a tile and goes on into the next one."""
+    counts = [390, 521, 16, 1000, 1, 64]
+    off, x, dy, _ = _inputs(counts, 1544, 1800, seed=9)
+    o, xd, dd = (t.to(cuda_dev) for t in (off, x, dy))
+    ws = torch.zeros(8192, dtype=torch.uint8, device=cuda_dev)
+    dw = moe.moe_grouped_mm_wgrad(dd, xd, o, out_dtype=F32, workspace=ws)
+    assert moe.moe_workspace_status(ws) == 0
+    ref, mag = wgrad64(dd, xd, off, device=cuda_dev)
+    for e in range(len(counts)):
+        check_sum(dw[e], ref[e].cpu(), mag[e].cpu(), counts[e], "expert %d" % e)
+    w = (torch.randn(len(counts), 1544, 1800, generator=torch.Generator().manual_seed(10)) * 0.1).to(BF).to(cuda_dev)
+    y, dx = moe.moe_grouped_mm(xd, o, w, workspace=ws), moe.moe_grouped_mm_dgrad(dd, o, w, workspace=ws)
+    assert moe.moe_workspace_status(ws) == 0
+    check_sum(y, *(t.cpu() for t in mm64(xd, off, w, False)), 1800, "forward")
+    check_sum(dx, *(t.cpu() for t in mm64(dd, off, w, True)), 1544, "input gradient")
+
+
 def test_same_bits_graph_and_streams(moe, cuda_dev):
     """Equal bits from repeated calls, from two streams that share a workspace,
     and from a captured graph replayed on new inputs; the status stays clean."""
