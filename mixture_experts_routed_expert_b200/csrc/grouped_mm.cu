@@ -29,9 +29,9 @@
 // Persistent: one CTA per SM, the pairs walk the tile list, which every CTA
 // derives from the offsets on the device.  Warp roles: 0 TMA producer of the
 // CTA's own operands (both CTAs' copies complete on the leading CTA's
-// barrier); 1 in the leading CTA MMA issue for the pair; 2-9 epilogue (two
-// sets of four warps, one warp per TMEM lane quarter, alternating 32
-// accumulator columns); 10 (weight gradient) zeroes the ragged end.
+// barrier); 1 in the leading CTA MMA issue for the pair; 2 on epilogue (two
+// sets of four warps, one warp per TMEM lane quarter, each set every other 32
+// accumulator columns); the last (weight gradient) zeroes the ragged end.
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -46,19 +46,20 @@ enum Op : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
 constexpr int kBK = 64;                        // reduction elements per stage = one 128-byte swizzle row
 constexpr int kTM = 256;                       // A-side width of a pair's tile
-constexpr int kEpiWarps = 8;
 constexpr int kABytes = kBM * 128;
 constexpr int kOutStage = 2 * 32 * kBM * 2;    // per epilogue set 32 rows x 128 columns of bf16
 constexpr int kChunkBytes = 64 * 128;          // MN-major: 64 elements x 64 reduction rows
-constexpr int kRaggedDelay = 3;                // k-blocks multiplied before a ragged one that was loaded first
+constexpr int kRaggedDelay = 1;                // k-blocks multiplied before a ragged one that was loaded first
 
 // BN: B-side width of a pair's tile; each CTA holds half of B.
-template <int OP, int BN>
+template <int OP, bool OUT_BF16, int BN>
 struct MmCfg {
     static constexpr int kStages = BN == 256 ? 6 : 9;
     static constexpr int kBBytes = BN / 2 * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kSets = kEpiWarps / 4;
     static constexpr int kThreads = 64 + 32 * kEpiWarps + (OP == kWgrad ? 32 : 0);
     static_assert(kRaggedDelay + 2 <= kStages && (OP != kWgrad || BN / 2 % 64 == 0), "");
     static size_t smem_bytes(int E) { return 1024 + kRingBytes + 1024 + kOutStage + align_up(12 * (size_t)(E + 1), 16); }
@@ -256,10 +257,10 @@ __device__ __forceinline__ bool ragged_end(const MmTile &t) {
 }
 
 template <int OP, bool OUT_BF16, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThreads), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16, BN>::kThreads), 1)
     grouped_mm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ ZeroMaps zero, const MmArgs args) {
-    using C = MmCfg<OP, BN>;
+    using C = MmCfg<OP, OUT_BF16, BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem;
@@ -290,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThr
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], 2 * kEpiWarps);
+            mbar_init(&tempty[a], 2 * C::kEpiWarps);
         }
         mbar_init(drained, 1);
         *abort_flag = 0;
@@ -341,7 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThr
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer ----
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t pol = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0;
@@ -479,14 +480,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThr
             }
             __syncwarp();
         }
-    } else if (OP == kWgrad && warp == 2 + kEpiWarps) {
+    } else if (OP == kWgrad && warp == 2 + C::kEpiWarps) {
         // ------------------------------------------------ ragged ends -----
         // In the last k-block of an expert the rows from `left` up to the end
         // of their 16-row step belong to the next expert: once the block has
         // landed, zero them in every 64-column chunk of this CTA's operands.
         // The block is loaded before the tile's others and multiplied after up
         // to kRaggedDelay of them, which hides the second trip.
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t pol = policy_evict_last();
             int stage = 0;
             uint32_t turn = 0;
@@ -542,10 +543,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThr
                 const float *p = args.base + at0 + (size_t)c0 * args.M;
                 if (c0 + 32 <= t.nrows) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = __ldcs(p);
+                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = *p;
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = c0 + j < t.nrows ? __ldcs(p) : 0.f;
+                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = c0 + j < t.nrows ? *p : 0.f;
                 }
             };
             read_base(set * 32);
@@ -567,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThr
                 if (lane == 0) mbar_arrive_leader(&tempty[acc]);
             };
             if (set * 32 >= t.nrows) release();
-            for (int c0 = set * 32; c0 < t.nrows; c0 += 64) {
+            for (int c0 = set * 32; c0 < t.nrows; c0 += 32 * C::kSets) {
                 uint32_t g[32];
                 if (none) {
 #pragma unroll
@@ -580,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThr
                     tmem_ld32(tb + c0, g);
                     tmem_ld_wait();
                 }
-                if (c0 + 64 >= t.nrows) release();
+                if (c0 + 32 * C::kSets >= t.nrows) release();
                 if (OUT_BF16) {
                     // g[h*16 + i*4 + o*2 + {0,1}]: TMEM lane h*16 + o*8 + lane/4, columns 8i + 2(lane%4) + {0,1}.
                     // Transposed 8x8 blocks to shared memory: row = accumulator column, 16-byte
@@ -603,26 +604,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, BN>::kThr
                         const int r = eg * 8 + i * 2 + (lane >> 4), u = lane & 15;
                         const uint4 v = ld_shared16(stg + r * (kBM * 2) + ((u ^ (r & 7)) << 4));
                         if (c0 + r < t.nrows && mc + u * 8 < args.M)
-                            __stcs(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(args.out) +
-                                                             (orow + c0 + r) * args.M + mc + u * 8), v);
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(args.out) +
+                                                       (orow + c0 + r) * args.M + mc + u * 8) = v;
                     }
                     named_barrier(1 + set, 128);
                 } else {
                     if (OP == kWgrad && args.base) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(__uint_as_float(g[j]) + b[j]);
-                        read_base(c0 + 64);
+                        read_base(c0 + 32 * C::kSets);
                     }
                     // one check a chunk: a compare, a branch and a 64-bit product a store
                     // made 600 instructions of a chunk and held the stores at 3 TB/s
                     float *o = static_cast<float *>(args.out) + at0 + (size_t)c0 * args.M;
                     if (mine && c0 + 32 <= t.nrows) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j, o += args.M) __stcs(o, __uint_as_float(g[j]));
+                        for (int j = 0; j < 32; ++j, o += args.M) *o = __uint_as_float(g[j]);
                     } else if (mine) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j, o += args.M)
-                            if (c0 + j < t.nrows) __stcs(o, __uint_as_float(g[j]));
+                            if (c0 + j < t.nrows) *o = __uint_as_float(g[j]);
                     }
                 }
             }
@@ -672,7 +673,7 @@ bool make_tmap_zero(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t col
 
 template <int OP, bool OUT_BF16, int BN>
 cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const ZeroMaps &z, const MmArgs &args, cudaStream_t st) {
-    using C = MmCfg<OP, BN>;
+    using C = MmCfg<OP, OUT_BF16, BN>;
     static std::atomic<int> attr_done[64];
     const cudaError_t e = enable_max_dyn_smem((const void *)grouped_mm<OP, OUT_BF16, BN>, attr_done);
     if (e != cudaSuccess) return e;
