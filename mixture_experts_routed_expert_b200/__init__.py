@@ -407,70 +407,82 @@ def moe_debug_permute(top_k_index, E, workspace=None, stream=None):
 # Tensors may live on any device: the call is made on the tensors' device, on
 # `stream` (default: that device's current stream).  With a stream given,
 # outputs are allocated on it and the inputs are recorded as in use by it.
+# The checks are kept lean: a step makes dozens of these calls, and the small
+# ones run for a few microseconds.
 
 _OTYPE = {torch.bfloat16: 0, torch.float32: 1}   # moe_otype_t
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _want(what, t, dtype, shape):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
 
 
 def _codes(what, t, shape):
-    if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+    if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
         raise TypeError("%s must be E4M3 codes (uint8 / float8_e4m3fn), got %s" % (what, t.dtype))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
 
 
-def _one_device(*tensors):
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.device != dev):
-            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
-    return dev
-
-
-def _new(shape, dtype, dev, stream):
+def _new(shape, dtype, like, stream):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _header_workspace(workspace, dev, stream):
+def _header_workspace(workspace, like, stream):
     """The caller's workspace (its size is checked by the library), or a fresh zeroed header."""
     if workspace is not None:
         return workspace
-    if stream is None:
-        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=dev)
+    if stream is None or not like.is_cuda:
+        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=dev)
+        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=like.device)
 
 
-def _enqueue(name, dev, stream, tensors, *args):
-    """Call entry point `name` with args and the stream, on device `dev`."""
+def _enqueue(name, stream, tensors, *rest):
+    """Call entry point `name` on the tensors' device and `stream`.  `tensors` (all of the call's, None for one
+    left out) are checked and become pointers: in `rest` an int argument stands for itself and _Ptr i for
+    tensors[i]."""
+    dev = tensors[0].get_device()
+    at = []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+        elif t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+        else:
+            at.append(t.data_ptr())
+    if dev < 0:
+        raise ValueError("all tensors must be contiguous CUDA tensors on one device")
     fn = getattr(_lib(), name)
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError("%s: the stream belongs to %s, the tensors to %s" % (name, stream.device, dev))
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream)
-    elif dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    args = [at[r] if type(r) is _Ptr else r for r in rest]
+    if stream is None and dev == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
+        if stream is not None:
+            if stream.device_index != dev:
+                raise ValueError("%s: the stream belongs to device %d, the tensors to %d" % (
+                    name, stream.device_index, dev))
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, name)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, name)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+class _Ptr(int):
+    """Place of a tensor in an _enqueue call's list."""
+
+
+_P = [_Ptr(i) for i in range(8)]
 
 
 def _out_type(out, out_dtype):
@@ -486,21 +498,19 @@ def _grouped(name, a, offsets, w, transpose, out, out_dtype, workspace, stream):
     E, N, C = w.shape
     rows = a.shape[0]
     ci, co = (N, C) if transpose else (C, N)
-    _want("the row matrix", a, torch.bfloat16, (rows, ci))
-    _want("w", w, torch.bfloat16, (E, N, C))
-    _want("offsets", offsets, torch.int32, (E + 1,))
+    _want("the row matrix", a, _BF16, (rows, ci))
+    _want("w", w, _BF16, (E, N, C))
+    _want("offsets", offsets, _I32, (E + 1,))
     if out is None and out_dtype is None:
-        out_dtype = torch.bfloat16
+        out_dtype = _BF16
     dt = _out_type(out, out_dtype)
-    dev = _one_device(a, offsets, w, out, workspace)
     if out is None:
-        out = _new((rows, co), dt, dev, stream)
+        out = _new((rows, co), dt, a, stream)
     else:
         _want("out", out, dt, (rows, co))
-    workspace = _header_workspace(workspace, dev, stream)
-    _enqueue(name, dev, stream, (a, offsets, w, out, workspace), a.data_ptr(), offsets.data_ptr(), w.data_ptr(),
-             rows, N, C, E, _OTYPE[dt], out.data_ptr(), workspace.data_ptr(),
-             workspace.numel() * workspace.element_size())
+    workspace = _header_workspace(workspace, a, stream)
+    _enqueue(name, stream, (a, offsets, w, out, workspace), _P[0], _P[1], _P[2], rows, N, C, E, _OTYPE[dt], _P[3],
+             _P[4], workspace.nbytes)
     return out
 
 
@@ -525,35 +535,33 @@ def moe_grouped_mm_wgrad(dy, x, offsets, base=None, out=None, out_dtype=None, wo
         raise ValueError("moe_grouped_mm_wgrad takes rows [rows, N] and [rows, C] and offsets [E+1]")
     rows, N = dy.shape
     C, E = x.shape[1], offsets.shape[0] - 1
-    _want("dy", dy, torch.bfloat16, (rows, N))
-    _want("x", x, torch.bfloat16, (rows, C))
-    _want("offsets", offsets, torch.int32, (E + 1,))
+    _want("dy", dy, _BF16, (rows, N))
+    _want("x", x, _BF16, (rows, C))
+    _want("offsets", offsets, _I32, (E + 1,))
     if out is None and out_dtype is None:
-        out_dtype = torch.bfloat16 if base is None else torch.float32
+        out_dtype = _BF16 if base is None else _F32
     dt = _out_type(out, out_dtype)
     if base is not None:
-        if dt != torch.float32:
+        if dt is not _F32:
             raise TypeError("base needs an fp32 output")
-        _want("base", base, torch.float32, (E, N, C))
-    dev = _one_device(dy, x, offsets, base, out, workspace)
+        _want("base", base, _F32, (E, N, C))
     if out is None:
-        out = _new((E, N, C), dt, dev, stream)
+        out = _new((E, N, C), dt, dy, stream)
     else:
         _want("out", out, dt, (E, N, C))
         if base is not None and base.data_ptr() != out.data_ptr() and \
-                abs(base.data_ptr() - out.data_ptr()) < 4 * out.numel():
+                abs(base.data_ptr() - out.data_ptr()) < out.nbytes:
             raise ValueError("base may be out itself, but must not overlap it otherwise")
-    workspace = _header_workspace(workspace, dev, stream)
-    _enqueue("moe_grouped_mm_wgrad", dev, stream, (dy, x, offsets, base, out, workspace), dy.data_ptr(),
-             x.data_ptr(), offsets.data_ptr(), rows, N, C, E, _OTYPE[dt], _at(base), out.data_ptr(),
-             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    workspace = _header_workspace(workspace, dy, stream)
+    _enqueue("moe_grouped_mm_wgrad", stream, (dy, x, offsets, base, out, workspace), _P[0], _P[1], _P[2], rows, N, C,
+             E, _OTYPE[dt], _P[3], _P[4], _P[5], workspace.nbytes)
     return out
 
 
 def _rows_args(row_weights, n_rows, rows):
     if row_weights is not None:
-        _want("row_weights", row_weights, torch.float32, (rows,))
-    if n_rows is not None and (n_rows.dtype != torch.int32 or n_rows.numel() != 1):
+        _want("row_weights", row_weights, _F32, (rows,))
+    if n_rows is not None and (n_rows.dtype is not _I32 or n_rows.numel() != 1):
         raise TypeError("n_rows must be one int32 on the device")
 
 
@@ -563,25 +571,24 @@ def moe_swiglu_checkpoint(gate_up, row_weights=None, n_rows=None, h=None, codes=
     offsets[-1:]): only the first n_rows rows are processed.  Returns (h, codes, scale)."""
     if gate_up.dim() != 2 or gate_up.shape[1] % 256:
         raise ValueError("gate_up must be [rows, 2F] with F a multiple of 128")
-    rows, F = gate_up.shape[0], gate_up.shape[1] // 2
-    _want("gate_up", gate_up, torch.bfloat16, (rows, 2 * F))
+    rows, F2 = gate_up.shape
+    F = F2 // 2
+    _want("gate_up", gate_up, _BF16, (rows, F2))
     _rows_args(row_weights, n_rows, rows)
-    dev = _one_device(gate_up, row_weights, n_rows, h, codes, scale)
     if h is None:
-        h = _new((rows, F), torch.bfloat16, dev, stream)
+        h = _new((rows, F), _BF16, gate_up, stream)
     else:
-        _want("h", h, torch.bfloat16, (rows, F))
+        _want("h", h, _BF16, (rows, F))
     if codes is None:
-        codes = _new((rows, 2 * F), torch.uint8, dev, stream)
+        codes = _new((rows, F2), torch.uint8, gate_up, stream)
     else:
-        _codes("codes", codes, (rows, 2 * F))
+        _codes("codes", codes, (rows, F2))
     if scale is None:
-        scale = _new((rows, F // 64), torch.float32, dev, stream)
+        scale = _new((rows, F // 64), _F32, gate_up, stream)
     else:
-        _want("scale", scale, torch.float32, (rows, F // 64))
-    _enqueue("moe_swiglu_checkpoint", dev, stream, (gate_up, row_weights, n_rows, h, codes, scale),
-             gate_up.data_ptr(), _at(row_weights), _at(n_rows), rows, F, h.data_ptr(), codes.data_ptr(),
-             scale.data_ptr())
+        _want("scale", scale, _F32, (rows, F // 64))
+    _enqueue("moe_swiglu_checkpoint", stream, (gate_up, row_weights, n_rows, h, codes, scale), _P[0], _P[1], _P[2],
+             rows, F, _P[3], _P[4], _P[5])
     return h, codes, scale
 
 
@@ -594,26 +601,25 @@ def moe_swiglu_checkpoint_backward(codes, scale, dh, row_weights=None, n_rows=No
     if dh.dim() != 2 or dh.shape[1] % 128:
         raise ValueError("dh must be [rows, F] with F a multiple of 128")
     rows, F = dh.shape
-    _want("dh", dh, torch.bfloat16, (rows, F))
+    _want("dh", dh, _BF16, (rows, F))
     _codes("codes", codes, (rows, 2 * F))
-    _want("scale", scale, torch.float32, (rows, F // 64))
+    _want("scale", scale, _F32, (rows, F // 64))
     _rows_args(row_weights, n_rows, rows)
-    dev = _one_device(dh, codes, scale, row_weights, n_rows, dgate_up, h, drow_weights)
     if dgate_up is None:
-        dgate_up = _new((rows, 2 * F), torch.bfloat16, dev, stream)
+        dgate_up = _new((rows, 2 * F), _BF16, dh, stream)
     else:
-        _want("dgate_up", dgate_up, torch.bfloat16, (rows, 2 * F))
+        _want("dgate_up", dgate_up, _BF16, (rows, 2 * F))
     if h is not None:
-        _want("h", h, torch.bfloat16, (rows, F))
+        _want("h", h, _BF16, (rows, F))
     elif want_h:
-        h = _new((rows, F), torch.bfloat16, dev, stream)
+        h = _new((rows, F), _BF16, dh, stream)
     if drow_weights is not None:
-        _want("drow_weights", drow_weights, torch.float32, (rows,))
+        _want("drow_weights", drow_weights, _F32, (rows,))
     elif want_drow_weights:
-        drow_weights = _new((rows,), torch.float32, dev, stream)
-    _enqueue("moe_swiglu_checkpoint_backward", dev, stream,
-             (codes, scale, dh, row_weights, n_rows, dgate_up, h, drow_weights), codes.data_ptr(), scale.data_ptr(),
-             dh.data_ptr(), _at(row_weights), _at(n_rows), rows, F, dgate_up.data_ptr(), _at(h), _at(drow_weights))
+        drow_weights = _new((rows,), _F32, dh, stream)
+    _enqueue("moe_swiglu_checkpoint_backward", stream,
+             (codes, scale, dh, row_weights, n_rows, dgate_up, h, drow_weights), _P[0], _P[1], _P[2], _P[3], _P[4],
+             rows, F, _P[5], _P[6], _P[7])
     return dgate_up, h, drow_weights
 
 
@@ -626,29 +632,29 @@ def moe_permute_rows(x, inv, top_k_weights=None, x_scale=None, out=None, row_wei
         raise ValueError("x must be [T, H] and inv [T, K]")
     T, H = x.shape
     K = inv.shape[1]
-    _want("inv", inv, torch.int32, (T, K))
+    _want("inv", inv, _I32, (T, K))
     if x_scale is None:
-        _want("x", x, torch.bfloat16, (T, H))
+        _want("x", x, _BF16, (T, H))
     else:
         _codes("x", x, (T, H))
-        _want("x_scale", x_scale, torch.float32, (T, H // 128))
+        _want("x_scale", x_scale, _F32, (T, H // 128))
     if top_k_weights is not None:
-        _want("top_k_weights", top_k_weights, torch.float32, (T, K))
+        _want("top_k_weights", top_k_weights, _F32, (T, K))
     elif row_weights is not None:
         raise ValueError("row_weights needs top_k_weights")
-    dev = _one_device(x, inv, top_k_weights, x_scale, out, row_weights)
-    n_rows = T * K if out is None else out.shape[0]
     if out is None:
-        out = _new((n_rows, H), torch.bfloat16, dev, stream)
+        n_rows = T * K
+        out = _new((n_rows, H), _BF16, x, stream)
     else:
-        _want("out", out, torch.bfloat16, (n_rows, H))
+        n_rows = out.shape[0]
+        _want("out", out, _BF16, (n_rows, H))
     if top_k_weights is not None:
         if row_weights is None:
-            row_weights = _new((n_rows,), torch.float32, dev, stream)
+            row_weights = _new((n_rows,), _F32, x, stream)
         else:
-            _want("row_weights", row_weights, torch.float32, (n_rows,))
-    _enqueue("moe_permute_rows", dev, stream, (x, inv, top_k_weights, x_scale, out, row_weights), x.data_ptr(),
-             _at(x_scale), inv.data_ptr(), _at(top_k_weights), K, T, H, n_rows, out.data_ptr(), _at(row_weights))
+            _want("row_weights", row_weights, _F32, (n_rows,))
+    _enqueue("moe_permute_rows", stream, (x, x_scale, inv, top_k_weights, out, row_weights), _P[0], _P[1], _P[2],
+             _P[3], K, T, H, n_rows, _P[4], _P[5])
     return out if row_weights is None else (out, row_weights)
 
 
@@ -662,24 +668,22 @@ def moe_unpermute_rows(y, inv, residual=None, drow_weights=None, out=None, dtop_
     T, K = inv.shape
     if y.dtype not in _OTYPE:
         raise TypeError("y must be bf16 or fp32, got %s" % y.dtype)
-    _want("inv", inv, torch.int32, (T, K))
+    _want("inv", inv, _I32, (T, K))
     if residual is not None:
-        _want("residual", residual, torch.bfloat16, (T, H))
+        _want("residual", residual, _BF16, (T, H))
     if drow_weights is not None:
-        _want("drow_weights", drow_weights, torch.float32, (n_rows,))
+        _want("drow_weights", drow_weights, _F32, (n_rows,))
     elif dtop_k_weights is not None:
         raise ValueError("dtop_k_weights needs drow_weights")
-    dev = _one_device(y, inv, residual, drow_weights, out, dtop_k_weights)
     if out is None:
-        out = _new((T, H), torch.bfloat16, dev, stream)
+        out = _new((T, H), _BF16, y, stream)
     else:
-        _want("out", out, torch.bfloat16, (T, H))
+        _want("out", out, _BF16, (T, H))
     if drow_weights is not None:
         if dtop_k_weights is None:
-            dtop_k_weights = _new((T, K), torch.float32, dev, stream)
+            dtop_k_weights = _new((T, K), _F32, y, stream)
         else:
-            _want("dtop_k_weights", dtop_k_weights, torch.float32, (T, K))
-    _enqueue("moe_unpermute_rows", dev, stream, (y, inv, residual, drow_weights, out, dtop_k_weights), y.data_ptr(),
-             _OTYPE[y.dtype], inv.data_ptr(), _at(residual), _at(drow_weights), K, T, H, n_rows, out.data_ptr(),
-             _at(dtop_k_weights))
+            _want("dtop_k_weights", dtop_k_weights, _F32, (T, K))
+    _enqueue("moe_unpermute_rows", stream, (y, inv, residual, drow_weights, out, dtop_k_weights), _P[0],
+             _OTYPE[y.dtype], _P[1], _P[2], _P[3], K, T, H, n_rows, _P[4], _P[5])
     return out if drow_weights is None else (out, dtop_k_weights)

@@ -362,4 +362,21 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4 q, float (&f)[8]) {
     f[4] = bf16_lo(q.z); f[5] = bf16_hi(q.z); f[6] = bf16_lo(q.w); f[7] = bf16_hi(q.w);
 }
 
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// 8 E4M3 codes times their block's scale.
+__device__ __forceinline__ void restore8_e4m3(const uint2 q, float scale, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t word = i < 2 ? q.x : q.y;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * (i & 1))), __NV_E4M3);
+        const float2 v = __half22float2(__half2(h));
+        f[2 * i] = v.x * scale;
+        f[2 * i + 1] = v.y * scale;
+    }
+}
+
 }  // namespace moe

@@ -15,100 +15,123 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 256;
+constexpr int kBatch = 4;      // slots of a token whose loads go out together
 
-__device__ __forceinline__ uint4 restore_bf16x8(const uint2 q, float scale) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t word = i < 2 ? q.x : q.y;
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * (i & 1))), __NV_E4M3);
-        const float2 v = __half22float2(__half2(h));
-        f[2 * i] = v.x * scale;
-        f[2 * i + 1] = v.y * scale;
-    }
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-}
-
-// One thread per (token, 8 columns).
+// A block holds blockDim.y tokens, blockDim.x threads each; a thread takes 8
+// columns at a time.
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads) permute_rows_kernel(
+__global__ void __launch_bounds__(kMaxThreads) permute_rows_kernel(
     const void *__restrict__ x, const float *__restrict__ x_scale, const int32_t *__restrict__ inv,
-    const float *__restrict__ weights, int64_t T, int K, int V, int n_out, uint4 *__restrict__ out,
+    const float *__restrict__ weights, int T, int K, int V, int n_out, uint4 *__restrict__ out,
     float *__restrict__ row_weights) {
-    const int64_t n = T * V;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t t = i / V;
-        const int c = (int)(i - t * V);
-        const uint4 v = FP8 ? restore_bf16x8(__ldg(static_cast<const uint2 *>(x) + i), __ldg(x_scale + t * (V / 16) + c / 16))
-                            : __ldg(static_cast<const uint4 *>(x) + i);
-        for (int k = 0; k < K; ++k) {
-            const int p = __ldg(inv + t * K + k);
-            if (p < 0 || p >= n_out) continue;
-            out[(int64_t)p * V + c] = v;
-            if (c == 0 && row_weights) row_weights[p] = __ldg(weights + t * K + k);
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.x * blockDim.y) {
+        const int32_t *pos = inv + t * K;
+        if (row_weights)
+            for (int k = threadIdx.x; k < K; k += blockDim.x) {
+                const int p = __ldg(pos + k);
+                if (p >= 0 && p < n_out) row_weights[p] = __ldg(weights + t * K + k);
+            }
+        for (int c = threadIdx.x; c < V; c += blockDim.x) {
+            uint4 v;
+            if (FP8) {
+                float f[8];
+                restore8_e4m3(__ldg(static_cast<const uint2 *>(x) + t * V + c), __ldg(x_scale + t * (V / 16) + c / 16), f);
+                v = pack_bf16x8(f);
+            } else {
+                v = __ldg(static_cast<const uint4 *>(x) + t * V + c);
+            }
+            for (int k = 0; k < K; ++k) {
+                const int p = __ldg(pos + k);
+                if (p >= 0 && p < n_out) out[(int64_t)p * V + c] = v;
+            }
         }
     }
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) unpermute_rows_kernel(
+__global__ void __launch_bounds__(kMaxThreads) unpermute_rows_kernel(
     const void *__restrict__ y, const int32_t *__restrict__ inv, const uint4 *__restrict__ residual,
-    const float *__restrict__ drow, int64_t T, int K, int V, int n_in, uint4 *__restrict__ out,
+    const float *__restrict__ drow, int T, int K, int V, int n_in, uint4 *__restrict__ out,
     float *__restrict__ dweights) {
-    const int64_t n = T * V;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t t = i / V;
-        const int c = (int)(i - t * V);
-        float acc[8] = {};
-        for (int k = 0; k < K; ++k) {
-            const int p = __ldg(inv + t * K + k);
-            const bool on = p >= 0 && p < n_in;
-            if (c == 0 && dweights) dweights[t * K + k] = on ? __ldg(drow + p) : 0.0f;
-            if (!on) continue;
-            float f[8];
-            if (F32) {
-                const float4 *q = static_cast<const float4 *>(y) + ((int64_t)p * V + c) * 2;
-                const float4 a = __ldg(q), b = __ldg(q + 1);
-                f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-                f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-            } else {
-                unpack_bf16x8(__ldg(static_cast<const uint4 *>(y) + (int64_t)p * V + c), f);
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.x * blockDim.y) {
+        const int32_t *pos = inv + t * K;
+        if (dweights)
+            for (int k = threadIdx.x; k < K; k += blockDim.x) {
+                const int p = __ldg(pos + k);
+                dweights[t * K + k] = p >= 0 && p < n_in ? __ldg(drow + p) : 0.0f;
             }
+        for (int c = threadIdx.x; c < V; c += blockDim.x) {
+            const uint4 vr = residual ? __ldg(residual + t * V + c) : make_uint4(0, 0, 0, 0);
+            float acc[8] = {};
+            for (int k0 = 0; k0 < K; k0 += kBatch) {
+                uint4 v[kBatch][F32 ? 2 : 1];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += f[j];
-        }
-        if (residual) {
-            float f[8];
-            unpack_bf16x8(__ldg(residual + i), f);
+                for (int j = 0; j < kBatch; ++j) {
+                    const int p = k0 + j < K ? __ldg(pos + k0 + j) : -1;
+                    const bool on = p >= 0 && p < n_in;      // a skipped slot adds zero
+                    const uint4 *q = static_cast<const uint4 *>(y) + ((int64_t)(on ? p : 0) * V + c) * (F32 ? 2 : 1);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += f[j];
+                    for (int i = 0; i < (F32 ? 2 : 1); ++i) v[j][i] = on ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    float f[8];
+                    if (F32) {
+                        f[0] = __uint_as_float(v[j][0].x); f[1] = __uint_as_float(v[j][0].y);
+                        f[2] = __uint_as_float(v[j][0].z); f[3] = __uint_as_float(v[j][0].w);
+                        f[4] = __uint_as_float(v[j][F32].x); f[5] = __uint_as_float(v[j][F32].y);
+                        f[6] = __uint_as_float(v[j][F32].z); f[7] = __uint_as_float(v[j][F32].w);
+                    } else {
+                        unpack_bf16x8(v[j][0], f);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] += f[i];
+                }
+            }
+            if (residual) {
+                float f[8];
+                unpack_bf16x8(vr, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += f[i];
+            }
+            out[t * V + c] = pack_bf16x8(acc);
         }
-        out[i] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-                            pack_bf16x2(acc[6], acc[7]));
     }
 }
 
-dim3 grid_of(int64_t n) {
-    return dim3((unsigned)std::min<int64_t>((n + kThreads - 1) / kThreads, 16LL * num_sms()));
+// Threads of a token: the fewest warps that go over its V vectors in
+// ceil(V / 256) rounds; a block holds as many tokens as fit in 256 threads.
+dim3 block_of(int V) {
+    const int rounds = (V + kMaxThreads - 1) / kMaxThreads;
+    const int tx = ((V + rounds - 1) / rounds + 31) / 32 * 32;
+    return dim3(tx, std::max(1, kMaxThreads / tx));
+}
+dim3 grid_of(int64_t T, dim3 block) {
+    return dim3((unsigned)std::min<int64_t>((T + block.y - 1) / block.y, 64LL * num_sms()));
 }
 
 }  // namespace
 
 cudaError_t launch_permute_rows(const void *x, const float *x_scale, const int32_t *inv, const float *weights,
                                 int64_t T, int K, int H, int n_out, void *out, float *row_weights, cudaStream_t st) {
+    const dim3 b = block_of(H / 8);
     auto *kernel = x_scale ? permute_rows_kernel<true> : permute_rows_kernel<false>;
-    return launch_k(kernel, grid_of(T * (H / 8)), dim3(kThreads), 0, st, false, x, x_scale, inv, weights, T, K, H / 8,
+    return launch_k(kernel, grid_of(T, b), b, 0, st, true, x, x_scale, inv, weights, (int)T, K, H / 8,
                     n_out, (uint4 *)out, row_weights);
 }
 
 cudaError_t launch_unpermute_rows(const void *y, bool y_fp32, const int32_t *inv, const void *residual,
                                   const float *drow, int64_t T, int K, int H, int n_in, void *out, float *dweights,
                                   cudaStream_t st) {
+    const dim3 b = block_of(H / 8);
     auto *kernel = y_fp32 ? unpermute_rows_kernel<true> : unpermute_rows_kernel<false>;
-    return launch_k(kernel, grid_of(T * (H / 8)), dim3(kThreads), 0, st, false, y, inv, (const uint4 *)residual, drow,
-                    T, K, H / 8, n_in, (uint4 *)out, dweights);
+    return launch_k(kernel, grid_of(T, b), b, 0, st, true, y, inv, (const uint4 *)residual, drow, (int)T, K,
+                    H / 8, n_in, (uint4 *)out, dweights);
 }
 
 }  // namespace moe

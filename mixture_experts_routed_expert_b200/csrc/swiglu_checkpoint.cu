@@ -45,90 +45,112 @@ __device__ __forceinline__ uint2 checkpoint8(const float (&f)[8], float &scale) 
     return q;
 }
 
-__device__ __forceinline__ void restore8(const uint2 q, float scale, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t word = i < 2 ? q.x : q.y;
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * (i & 1))), __NV_E4M3);
-        const float2 v = __half22float2(__half2(h));
-        f[2 * i] = v.x * scale;
-        f[2 * i + 1] = v.y * scale;
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-}
-
 // Rows to process: the device's count when there is one, within the buffers.
 __device__ __forceinline__ int64_t live_rows(const int32_t *n_rows, int rows) {
     return n_rows ? min(max(__ldg(n_rows), 0), rows) : rows;
 }
 
-// One lane per 8 features of a row.
+// Half a warp per block of 128 features (gate and up), 8 values a lane; the
+// half-warps stride over the (row, block) pairs, stepping both parts of the
+// index (a 64-bit division per pair cost a quarter of the kernel).
 __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(
     const uint4 *__restrict__ gu, const float *__restrict__ weight, const int32_t *__restrict__ n_rows, int rows,
     int F, uint4 *__restrict__ h, uint2 *__restrict__ codes, float *__restrict__ scale) {
-    const int V = F / 8;
-    const int64_t n = live_rows(n_rows, rows) * V;
-    for (int64_t v0 = (int64_t)blockIdx.x * kThreads; v0 < n; v0 += (int64_t)gridDim.x * kThreads) {
-        const int64_t v = v0 + threadIdx.x;
-        const bool on = v < n;
-        const int64_t r = on ? v / V : 0;
-        const int c = on ? (int)(v - r * V) : 0;
-        float g[8], u[8], o[8];
-        unpack_bf16x8(on ? __ldg(gu + r * 2 * V + c) : make_uint4(0, 0, 0, 0), g);
-        unpack_bf16x8(on ? __ldg(gu + r * 2 * V + V + c) : make_uint4(0, 0, 0, 0), u);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int NB = F / 128, V = F / 8, sub = threadIdx.x & 15;
+    const int64_t live = live_rows(n_rows, rows);
+    const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
+    const int64_t stride = ((int64_t)gridDim.x * kThreads) >> 4;
+    const int64_t step_r = stride / NB;
+    const int step_b = (int)(stride - step_r * NB);
+    int64_t r = first / NB;
+    int b = (int)(first - r * NB);
+    // the two halves of a warp stay together: the block scale is found by warp shuffles
+    while (__any_sync(0xFFFFFFFFu, r < live)) {
+        const bool on = r < live;
+        const int64_t at = r * 2 * V + b * 16 + sub;
+        const uint4 vg = on ? __ldg(gu + at) : make_uint4(0, 0, 0, 0);
+        const uint4 vu = on ? __ldg(gu + at + V) : make_uint4(0, 0, 0, 0);
         const float p = weight && on ? __ldg(weight + r) : 1.0f;
+        float g[8], u[8], o[8];
+        unpack_bf16x8(vg, g);
+        unpack_bf16x8(vu, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = p * (g[i] * sigmoid_f(g[i]) * u[i]);
         float sg, su;
-        const uint2 qg = checkpoint8(g, sg), qu = checkpoint8(u, su);   // every lane of the warp takes part
+        const uint2 qg = checkpoint8(g, sg), qu = checkpoint8(u, su);
         if (on) {
-            h[r * V + c] = pack8(o);
-            codes[r * 2 * V + c] = qg;
-            codes[r * 2 * V + V + c] = qu;
-            if ((c & 15) == 0) {
-                scale[r * (2 * V / 16) + c / 16] = sg;
-                scale[r * (2 * V / 16) + V / 16 + c / 16] = su;
-            }
+            h[r * V + b * 16 + sub] = pack_bf16x8(o);
+            codes[at] = qg;
+            codes[at + V] = qu;
+            if (sub < 2) scale[r * 2 * NB + sub * NB + b] = sub ? su : sg;
+        }
+        r += step_r;
+        b += step_b;
+        if (b >= NB) {
+            b -= NB;
+            ++r;
         }
     }
 }
 
-// One warp per row.
+// WPR warps per row: one for many rows, four for few (the row's loads then
+// all go out at once).
+template <int WPR>
 __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_backward_kernel(
     const uint2 *__restrict__ codes, const float *__restrict__ scale, const uint4 *__restrict__ dh,
     const float *__restrict__ weight, const int32_t *__restrict__ n_rows, int rows, int F, uint4 *__restrict__ dgu,
     uint4 *__restrict__ h, float *__restrict__ dweight) {
-    const int V = F / 8, lane = lane_id();
-    const int64_t n = live_rows(n_rows, rows);
-    for (int64_t r = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < n;
-         r += (int64_t)gridDim.x * (kThreads / 32)) {
-        const float p = weight ? __ldg(weight + r) : 1.0f;
+    __shared__ float s_dot[kThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int NB = F / 128, V = F / 8, lane = lane_id(), warp = threadIdx.x >> 5;
+    const int64_t live = live_rows(n_rows, rows);
+    const int64_t stride = (int64_t)gridDim.x * (kThreads / 32 / WPR);
+    for (int64_t r0 = (int64_t)blockIdx.x * (kThreads / 32 / WPR); r0 < live; r0 += stride) {
+        const int64_t r = r0 + warp / WPR;
         float dot = 0.f;
-        for (int c = lane; c < V; c += 32) {
-            float g[8], u[8], d[8], dg[8], du[8], o[8];
-            restore8(__ldg(codes + r * 2 * V + c), __ldg(scale + r * (2 * V / 16) + c / 16), g);
-            restore8(__ldg(codes + r * 2 * V + V + c), __ldg(scale + r * (2 * V / 16) + (V + c) / 16), u);
-            unpack_bf16x8(__ldg(dh + r * V + c), d);
+        if (r < live) {
+            const float p = weight ? __ldg(weight + r) : 1.0f;
+            const uint2 *cr = codes + r * 2 * V;
+            const float *sr = scale + r * 2 * NB;
+            const uint4 *dr = dh + r * V;
+            uint4 *gr = dgu + r * 2 * V, *hr = h ? h + r * V : nullptr;
+#pragma unroll 2
+            for (int c = (warp % WPR) * 32 + lane; c < V; c += 32 * WPR) {
+                float g[8], u[8], d[8], dg[8], du[8], o[8];
+                restore8_e4m3(__ldg(cr + c), __ldg(sr + c / 16), g);
+                restore8_e4m3(__ldg(cr + V + c), __ldg(sr + NB + c / 16), u);
+                unpack_bf16x8(__ldg(dr + c), d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = sigmoid_f(g[i]), a = g[i] * s, pd = p * d[i];
-                dot += d[i] * (a * u[i]);
-                o[i] = p * (a * u[i]);
-                dg[i] = pd * u[i] * (s + a * (1.0f - s));
-                du[i] = pd * a;
+                for (int i = 0; i < 8; ++i) {
+                    const float s = sigmoid_f(g[i]), a = g[i] * s, pd = p * d[i], au = a * u[i];
+                    dot += d[i] * au;
+                    o[i] = p * au;
+                    dg[i] = pd * u[i] * (s + a * (1.0f - s));
+                    du[i] = pd * a;
+                }
+                gr[c] = pack_bf16x8(dg);
+                gr[V + c] = pack_bf16x8(du);
+                if (hr) hr[c] = pack_bf16x8(o);
             }
-            dgu[r * 2 * V + c] = pack8(dg);
-            dgu[r * 2 * V + V + c] = pack8(du);
-            if (h) h[r * V + c] = pack8(o);
         }
         if (dweight) {
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-            if (lane == 0) dweight[r] = dot;
+            if (WPR == 1) {
+                if (lane == 0 && r < live) dweight[r] = dot;
+            } else {
+                if (lane == 0) s_dot[warp] = dot;
+                __syncthreads();
+                if (lane == 0 && warp % WPR == 0 && r < live) {
+                    float sum = s_dot[warp];
+                    for (int i = 1; i < WPR; ++i) sum += s_dot[warp + i];
+                    dweight[r] = sum;
+                }
+                __syncthreads();
+            }
         }
     }
 }
@@ -139,17 +161,20 @@ cudaError_t launch_swiglu_checkpoint(const void *gu, const float *weight, const 
                                      void *h, void *codes, float *scale, cudaStream_t st) {
     const int64_t blocks = ((int64_t)rows * (F / 8) + kThreads - 1) / kThreads;
     return launch_k(swiglu_checkpoint_kernel, dim3((unsigned)std::min<int64_t>(blocks, 8LL * num_sms())),
-                    dim3(kThreads), 0, st, false, (const uint4 *)gu, weight, n_rows, rows, F, (uint4 *)h,
+                    dim3(kThreads), 0, st, true, (const uint4 *)gu, weight, n_rows, rows, F, (uint4 *)h,
                     (uint2 *)codes, scale);
 }
 
 cudaError_t launch_swiglu_checkpoint_backward(const void *codes, const float *scale, const void *dh,
                                               const float *weight, const int32_t *n_rows, int rows, int F, void *dgu,
                                               void *h, float *dweight, cudaStream_t st) {
-    const int64_t blocks = ((int64_t)rows + kThreads / 32 - 1) / (kThreads / 32);
-    return launch_k(swiglu_checkpoint_backward_kernel, dim3((unsigned)std::min<int64_t>(blocks, 8LL * num_sms())),
-                    dim3(kThreads), 0, st, false, (const uint2 *)codes, scale, (const uint4 *)dh, weight, n_rows, rows,
-                    F, (uint4 *)dgu, (uint4 *)h, dweight);
+    const bool few = rows <= 8 * num_sms();
+    const int per_block = kThreads / 32 / (few ? 4 : 1);
+    const int64_t blocks = ((int64_t)rows + per_block - 1) / per_block;
+    auto *kernel = few ? swiglu_checkpoint_backward_kernel<4> : swiglu_checkpoint_backward_kernel<1>;
+    return launch_k(kernel, dim3((unsigned)std::min<int64_t>(blocks, 8LL * num_sms())), dim3(kThreads), 0, st, true,
+                    (const uint2 *)codes, scale, (const uint4 *)dh, weight, n_rows, rows, F, (uint4 *)dgu, (uint4 *)h,
+                    dweight);
 }
 
 }  // namespace moe
