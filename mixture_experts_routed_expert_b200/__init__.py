@@ -445,44 +445,33 @@ def _header_workspace(workspace, like, stream):
         return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=like.device)
 
 
-def _enqueue(name, stream, tensors, *rest):
-    """Call entry point `name` on the tensors' device and `stream`.  `tensors` (all of the call's, None for one
-    left out) are checked and become pointers: in `rest` an int argument stands for itself and _Ptr i for
-    tensors[i]."""
-    dev = tensors[0].get_device()
+def _enqueue(name, stream, *args):
+    """Call entry point `name` with `args` (tensors, integers or None, in the library's order; the first is a
+    tensor) and the stream, on the tensors' device."""
+    dev = args[0].get_device()
     at = []
-    for t in tensors:
-        if t is None:
-            at.append(None)
-        elif t.get_device() != dev or not t.is_contiguous():
+    for a in args:
+        if type(a) is int or a is None:
+            at.append(a)
+        elif a.get_device() != dev or not a.is_contiguous() or dev < 0:
             raise ValueError("all tensors must be contiguous CUDA tensors on one device")
         else:
-            at.append(t.data_ptr())
-    if dev < 0:
-        raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+            at.append(a.data_ptr())
     fn = getattr(_lib(), name)
-    args = [at[r] if type(r) is _Ptr else r for r in rest]
-    if stream is None and dev == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if stream is None and dev == torch._C._cuda_getDevice():
+        rc = fn(*at, torch._C._cuda_getCurrentRawStream(dev))
     else:
         if stream is not None:
             if stream.device_index != dev:
                 raise ValueError("%s: the stream belongs to device %d, the tensors to %d" % (
                     name, stream.device_index, dev))
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
+            for a in args:
+                if isinstance(a, torch.Tensor):
+                    a.record_stream(stream)
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+            rc = fn(*at, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, name)
-
-
-class _Ptr(int):
-    """Place of a tensor in an _enqueue call's list."""
-
-
-_P = [_Ptr(i) for i in range(8)]
 
 
 def _out_type(out, out_dtype):
@@ -498,19 +487,20 @@ def _grouped(name, a, offsets, w, transpose, out, out_dtype, workspace, stream):
     E, N, C = w.shape
     rows = a.shape[0]
     ci, co = (N, C) if transpose else (C, N)
-    _want("the row matrix", a, _BF16, (rows, ci))
-    _want("w", w, _BF16, (E, N, C))
-    _want("offsets", offsets, _I32, (E + 1,))
+    if a.dtype is not _BF16 or w.dtype is not _BF16 or offsets.dtype is not _I32 or a.shape[1] != ci or \
+            offsets.shape != (E + 1,):
+        _want("the row matrix", a, _BF16, (rows, ci))
+        _want("w", w, _BF16, (E, N, C))
+        _want("offsets", offsets, _I32, (E + 1,))
     if out is None and out_dtype is None:
         out_dtype = _BF16
     dt = _out_type(out, out_dtype)
     if out is None:
         out = _new((rows, co), dt, a, stream)
-    else:
+    elif out.shape != (rows, co):
         _want("out", out, dt, (rows, co))
     workspace = _header_workspace(workspace, a, stream)
-    _enqueue(name, stream, (a, offsets, w, out, workspace), _P[0], _P[1], _P[2], rows, N, C, E, _OTYPE[dt], _P[3],
-             _P[4], workspace.nbytes)
+    _enqueue(name, stream, a, offsets, w, rows, N, C, E, _OTYPE[dt], out, workspace, workspace.nbytes)
     return out
 
 
@@ -553,8 +543,8 @@ def moe_grouped_mm_wgrad(dy, x, offsets, base=None, out=None, out_dtype=None, wo
                 abs(base.data_ptr() - out.data_ptr()) < out.nbytes:
             raise ValueError("base may be out itself, but must not overlap it otherwise")
     workspace = _header_workspace(workspace, dy, stream)
-    _enqueue("moe_grouped_mm_wgrad", stream, (dy, x, offsets, base, out, workspace), _P[0], _P[1], _P[2], rows, N, C,
-             E, _OTYPE[dt], _P[3], _P[4], _P[5], workspace.nbytes)
+    _enqueue("moe_grouped_mm_wgrad", stream, dy, x, offsets, rows, N, C, E, _OTYPE[dt], base, out, workspace,
+             workspace.nbytes)
     return out
 
 
@@ -587,8 +577,7 @@ def moe_swiglu_checkpoint(gate_up, row_weights=None, n_rows=None, h=None, codes=
         scale = _new((rows, F // 64), _F32, gate_up, stream)
     else:
         _want("scale", scale, _F32, (rows, F // 64))
-    _enqueue("moe_swiglu_checkpoint", stream, (gate_up, row_weights, n_rows, h, codes, scale), _P[0], _P[1], _P[2],
-             rows, F, _P[3], _P[4], _P[5])
+    _enqueue("moe_swiglu_checkpoint", stream, gate_up, row_weights, n_rows, rows, F, h, codes, scale)
     return h, codes, scale
 
 
@@ -617,9 +606,8 @@ def moe_swiglu_checkpoint_backward(codes, scale, dh, row_weights=None, n_rows=No
         _want("drow_weights", drow_weights, _F32, (rows,))
     elif want_drow_weights:
         drow_weights = _new((rows,), _F32, dh, stream)
-    _enqueue("moe_swiglu_checkpoint_backward", stream,
-             (codes, scale, dh, row_weights, n_rows, dgate_up, h, drow_weights), _P[0], _P[1], _P[2], _P[3], _P[4],
-             rows, F, _P[5], _P[6], _P[7])
+    _enqueue("moe_swiglu_checkpoint_backward", stream, codes, scale, dh, row_weights, n_rows, rows, F, dgate_up, h,
+             drow_weights)
     return dgate_up, h, drow_weights
 
 
@@ -653,8 +641,7 @@ def moe_permute_rows(x, inv, top_k_weights=None, x_scale=None, out=None, row_wei
             row_weights = _new((n_rows,), _F32, x, stream)
         else:
             _want("row_weights", row_weights, _F32, (n_rows,))
-    _enqueue("moe_permute_rows", stream, (x, x_scale, inv, top_k_weights, out, row_weights), _P[0], _P[1], _P[2],
-             _P[3], K, T, H, n_rows, _P[4], _P[5])
+    _enqueue("moe_permute_rows", stream, x, x_scale, inv, top_k_weights, K, T, H, n_rows, out, row_weights)
     return out if row_weights is None else (out, row_weights)
 
 
@@ -684,6 +671,6 @@ def moe_unpermute_rows(y, inv, residual=None, drow_weights=None, out=None, dtop_
             dtop_k_weights = _new((T, K), _F32, y, stream)
         else:
             _want("dtop_k_weights", dtop_k_weights, _F32, (T, K))
-    _enqueue("moe_unpermute_rows", stream, (y, inv, residual, drow_weights, out, dtop_k_weights), _P[0],
-             _OTYPE[y.dtype], _P[1], _P[2], _P[3], K, T, H, n_rows, _P[4], _P[5])
+    _enqueue("moe_unpermute_rows", stream, y, _OTYPE[y.dtype], inv, residual, drow_weights, K, T, H, n_rows, out,
+             dtop_k_weights)
     return out if drow_weights is None else (out, dtop_k_weights)

@@ -299,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
     }
-    if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+    if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * BN);
     pdl_wait();
     // Row ranges of the experts, clamped into the matrices whatever the
     // offsets hold, and the prefix sum of their row tiles: each thread sums a
@@ -638,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, 512);
+        tmem_dealloc_pair(tmem_base, 2 * BN);
     }
 }
 
@@ -699,7 +699,7 @@ cudaError_t launch_grouped_mm(const void *x, const void *w, const int32_t *offse
     a.M = transpose ? C : N;
     a.red = red;
     const bool few = rows <= (int64_t)32 * E;
-    a.box_rows = few ? 32 : 128;
+    a.box_rows = few ? 32 : 128;   // at most BN / 2: the boxes of a stage lie within its B region
     a.out = out;
     a.status = status;
     CUtensorMap ta, tb;

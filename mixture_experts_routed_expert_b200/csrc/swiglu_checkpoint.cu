@@ -23,26 +23,102 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+// Blocks in the grid per SM, about eight resident: more, shorter blocks keep
+// neighbouring rows together in time (65536 x 2048 forward, 8 / 32 / 128 per
+// SM: 192 / 178 / 180 us).
+constexpr int kBlocksPerSm = 32;
 
-__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
+// ---- two fp32 values per instruction ---------------------------------------
+// The kernels issue as many instructions as the memory allows them time for,
+// so sums and products go two at a time.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 unpack2(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
 
-// Block scale and codes of 8 values per lane, 16 lanes per block of 128, as
-// quant8_e4m3; a block that holds an infinity takes the exponent of the
-// largest finite value, whose largest code is restored as an infinity (448 *
-// 2^120 overflows), and a NaN keeps its own code.
-__device__ __forceinline__ uint2 checkpoint8(const float (&f)[8], float &scale) {
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const int k = fp8_block_exp(fminf(amax, FLT_MAX));
+// 1 / (1 + 2^(-g log2 e)): relative error at most (|g| + 8) 2^-24 (the rounded
+// argument, the two approximations and the sum), 0 once 2^(-g log2 e) overflows.
+__device__ __forceinline__ F2 sigmoid2(F2 g) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    float a, b;
+    split(g * f2(-kLog2e, -kLog2e), a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    split(f2(a, b) + f2(1.0f, 1.0f), a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2(a, b);
+}
+
+// ---- 8-bit blocks -----------------------------------------------------------
+// Largest magnitude among 8 packed bf16 values, as the value's 15 bits (NaN
+// does not count).
+__device__ __forceinline__ uint32_t amax8(const uint4 &q) {
+    auto mag = [](uint32_t w) {
+        w &= 0x7FFF7FFFu;
+        return *reinterpret_cast<__nv_bfloat162 *>(&w);
+    };
+    const __nv_bfloat162 m = __hmax2(__hmax2(mag(q.x), mag(q.y)), __hmax2(mag(q.z), mag(q.w)));
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
+    const __nv_bfloat162 h = __hmax2(m, mag(w >> 16));
+    return *reinterpret_cast<const uint32_t *>(&h) & 0xFFFFu;
+}
+// The rule of fp8_block_exp on a magnitude's bits: amax = f 2^e with f in
+// [0.5, 1) has k = e - 9, or e - 8 for f > 0.875 (mantissa bits above 0x60),
+// clamped below at -127; an infinity (or no number at all) counts as the
+// largest finite value, whose largest code is restored as an infinity
+// (448 * 2^120 overflows).
+__device__ __forceinline__ int block_exp(uint32_t bits) {
+    bits = min(bits, 0x7F7Fu);
+    return bits == 0 ? 0 : max(-127, (int)((bits + 0x1Fu) >> 7) - 135);
+}
+// 8 bf16 values times 2^-k as E4M3 codes.
+__device__ __forceinline__ uint2 codes8(const F2 (&f)[4], int k) {
     const float inv = pow2f(-k);
-    scale = pow2f(k);
-    uint2 q;
-    q.x = (uint32_t)e4m3x2(f[0] * inv, f[1] * inv) | ((uint32_t)e4m3x2(f[2] * inv, f[3] * inv) << 16);
-    q.y = (uint32_t)e4m3x2(f[4] * inv, f[5] * inv) | ((uint32_t)e4m3x2(f[6] * inv, f[7] * inv) << 16);
-    return q;
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        split(f[i] * f2(inv, inv), lo, hi);
+        c[i] = e4m3x2(lo, hi);
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+// 8 E4M3 codes times their block's scale.
+__device__ __forceinline__ void restore8(const uint2 q, float scale, F2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t word = i < 2 ? q.x : q.y;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * (i & 1))), __NV_E4M3);
+        const float2 v = __half22float2(__half2(h));
+        f[i] = f2(v.x, v.y) * f2(scale, scale);
+    }
 }
 
 // Rows to process: the device's count when there is one, within the buffers.
@@ -73,18 +149,26 @@ __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(
         const uint4 vg = on ? __ldg(gu + at) : make_uint4(0, 0, 0, 0);
         const uint4 vu = on ? __ldg(gu + at + V) : make_uint4(0, 0, 0, 0);
         const float p = weight && on ? __ldg(weight + r) : 1.0f;
-        float g[8], u[8], o[8];
-        unpack_bf16x8(vg, g);
-        unpack_bf16x8(vu, u);
+        // both maxima of the block in one word through the half-warp's shuffles
+        uint32_t m = amax8(vg) | (amax8(vu) << 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = p * (g[i] * sigmoid_f(g[i]) * u[i]);
-        float sg, su;
-        const uint2 qg = checkpoint8(g, sg), qu = checkpoint8(u, su);
+        for (int o = 8; o >= 1; o >>= 1) {
+            const uint32_t w = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+            const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&w));
+            m = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        const int kg = block_exp(m & 0xFFFFu), ku = block_exp(m >> 16);
+        const F2 g[4] = {unpack2(vg.x), unpack2(vg.y), unpack2(vg.z), unpack2(vg.w)};
+        const F2 u[4] = {unpack2(vu.x), unpack2(vu.y), unpack2(vu.z), unpack2(vu.w)};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack2(f2(p, p) * (g[i] * sigmoid2(g[i]) * u[i]));
         if (on) {
-            h[r * V + b * 16 + sub] = pack_bf16x8(o);
-            codes[at] = qg;
-            codes[at + V] = qu;
-            if (sub < 2) scale[r * 2 * NB + sub * NB + b] = sub ? su : sg;
+            h[r * V + b * 16 + sub] = make_uint4(o[0], o[1], o[2], o[3]);
+            codes[at] = codes8(g, kg);
+            codes[at + V] = codes8(u, ku);
+            if (sub < 2) scale[r * 2 * NB + sub * NB + b] = pow2f(sub ? ku : kg);
         }
         r += step_r;
         b += step_b;
@@ -98,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(
 // WPR warps per row: one for many rows, four for few (the row's loads then
 // all go out at once).
 template <int WPR>
-__global__ void __launch_bounds__(kThreads) swiglu_checkpoint_backward_kernel(
+__global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel(
     const uint2 *__restrict__ codes, const float *__restrict__ scale, const uint4 *__restrict__ dh,
     const float *__restrict__ weight, const int32_t *__restrict__ n_rows, int rows, int F, uint4 *__restrict__ dgu,
     uint4 *__restrict__ h, float *__restrict__ dweight) {
@@ -117,24 +201,43 @@ __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_backward_kernel(
             const float *sr = scale + r * 2 * NB;
             const uint4 *dr = dh + r * V;
             uint4 *gr = dgu + r * 2 * V, *hr = h ? h + r * V : nullptr;
-#pragma unroll 2
-            for (int c = (warp % WPR) * 32 + lane; c < V; c += 32 * WPR) {
-                float g[8], u[8], d[8], dg[8], du[8], o[8];
-                restore8_e4m3(__ldg(cr + c), __ldg(sr + c / 16), g);
-                restore8_e4m3(__ldg(cr + V + c), __ldg(sr + NB + c / 16), u);
-                unpack_bf16x8(__ldg(dr + c), d);
+            F2 dot2 = f2(0.f, 0.f);
+            int c = (warp % WPR) * 32 + lane;
+            uint2 qg = make_uint2(0, 0), qu = qg;
+            uint4 vd = make_uint4(0, 0, 0, 0);
+            float sg = 0.f, su = 0.f;
+            auto load = [&](int at) {      // a step ahead of the arithmetic
+                if (at >= V) return;
+                qg = __ldg(cr + at);
+                qu = __ldg(cr + V + at);
+                sg = __ldg(sr + at / 16);
+                su = __ldg(sr + NB + at / 16);
+                vd = __ldg(dr + at);
+            };
+            load(c);
+            for (; c < V; c += 32 * WPR) {
+                F2 g[4], u[4];
+                restore8(qg, sg, g);
+                restore8(qu, su, u);
+                const F2 d[4] = {unpack2(vd.x), unpack2(vd.y), unpack2(vd.z), unpack2(vd.w)};
+                load(c + 32 * WPR);
+                uint32_t dg[4], du[4], o[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float s = sigmoid_f(g[i]), a = g[i] * s, pd = p * d[i], au = a * u[i];
-                    dot += d[i] * au;
-                    o[i] = p * au;
-                    dg[i] = pd * u[i] * (s + a * (1.0f - s));
-                    du[i] = pd * a;
+                for (int i = 0; i < 4; ++i) {
+                    const F2 s = sigmoid2(g[i]), a = g[i] * s, pd = f2(p, p) * d[i], au = a * u[i];
+                    dot2 = fma2(d[i], au, dot2);
+                    o[i] = pack2(f2(p, p) * au);
+                    const F2 rest = fma2(s, f2(-1.f, -1.f), f2(1.f, 1.f));      // 1 - s
+                    dg[i] = pack2(pd * u[i] * fma2(a, rest, s));
+                    du[i] = pack2(pd * a);
                 }
-                gr[c] = pack_bf16x8(dg);
-                gr[V + c] = pack_bf16x8(du);
-                if (hr) hr[c] = pack_bf16x8(o);
+                gr[c] = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+                gr[V + c] = make_uint4(du[0], du[1], du[2], du[3]);
+                if (hr) hr[c] = make_uint4(o[0], o[1], o[2], o[3]);
             }
+            float lo, hi;
+            split(dot2, lo, hi);
+            dot = lo + hi;
         }
         if (dweight) {
 #pragma unroll
@@ -160,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_checkpoint_backward_kernel(
 cudaError_t launch_swiglu_checkpoint(const void *gu, const float *weight, const int32_t *n_rows, int rows, int F,
                                      void *h, void *codes, float *scale, cudaStream_t st) {
     const int64_t blocks = ((int64_t)rows * (F / 8) + kThreads - 1) / kThreads;
-    return launch_k(swiglu_checkpoint_kernel, dim3((unsigned)std::min<int64_t>(blocks, 8LL * num_sms())),
+    return launch_k(swiglu_checkpoint_kernel, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)kBlocksPerSm * num_sms())),
                     dim3(kThreads), 0, st, true, (const uint4 *)gu, weight, n_rows, rows, F, (uint4 *)h,
                     (uint2 *)codes, scale);
 }
@@ -172,7 +275,7 @@ cudaError_t launch_swiglu_checkpoint_backward(const void *codes, const float *sc
     const int per_block = kThreads / 32 / (few ? 4 : 1);
     const int64_t blocks = ((int64_t)rows + per_block - 1) / per_block;
     auto *kernel = few ? swiglu_checkpoint_backward_kernel<4> : swiglu_checkpoint_backward_kernel<1>;
-    return launch_k(kernel, dim3((unsigned)std::min<int64_t>(blocks, 8LL * num_sms())), dim3(kThreads), 0, st, true,
+    return launch_k(kernel, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)kBlocksPerSm * num_sms())), dim3(kThreads), 0, st, true,
                     (const uint2 *)codes, scale, (const uint4 *)dh, weight, n_rows, rows, F, (uint4 *)dgu, (uint4 *)h,
                     dweight);
 }

@@ -1,0 +1,123 @@
+"""Forward and backward of the routed-experts layer for training, out of the
+library's operators (bf16 weights; the pages describe the forward only).
+
+Forward, with N = T*K routing slots in expert order:
+
+  plan        offsets [E+1] and the position of every slot (moe_debug_permute)
+  permute     xp = x by slot, p = router weights by slot
+  gate/up     gu = xp gate_up^T per expert             (moe_grouped_mm)
+  activation  h = p silu(g) u, and g, u kept in 8 bits (moe_swiglu_checkpoint)
+  down        y = h down^T per expert                  (moe_grouped_mm)
+  combine     out = sum of a token's K rows (+ residual)
+
+Backward from the output's gradient:
+
+  dy = dout by slot;  dh = dy down                     (moe_grouped_mm_dgrad)
+  dgu, h, dp from the 8-bit checkpoint                 (moe_swiglu_checkpoint_backward)
+  ddown = dy^T h,  dgate_up = dgu^T xp per expert      (moe_grouped_mm_wgrad)
+  dx = sum over a token's slots of dgu gate_up,  dtop_k_weights = dp by slot
+
+What is kept between the two is x (bf16, or 8 bits with keep_x="e4m3"), the
+plan, the router weights by slot and the 8-bit checkpoint: 2F bytes a slot
+and F/32 of scales, where gu and h in bf16 would be 6F.  The router weight is
+applied before the down product, so its gradient is a dot product over F and
+y need not be kept.
+
+The functions only enqueue work on the current stream of the tensors' device
+and can be captured into a CUDA graph.  Slots whose id is outside [0, E)
+contribute nothing and get zero gradients.
+"""
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import (moe_debug_permute, moe_grouped_mm, moe_grouped_mm_dgrad, moe_grouped_mm_wgrad, moe_permute_rows,
+               moe_swiglu_checkpoint, moe_swiglu_checkpoint_backward, moe_unpermute_rows, quantize_fp8_block128)
+
+
+@dataclass
+class ExpertsSaved:
+    """What experts_forward keeps for experts_backward."""
+    offsets: torch.Tensor               # [E+1] int32
+    inv: torch.Tensor                   # [T,K] int32
+    codes: torch.Tensor                 # [N,2F] uint8, E4M3 gate | up
+    scale: torch.Tensor                 # [N,2F/128] fp32
+    row_weights: torch.Tensor           # [N] fp32
+    x: torch.Tensor                     # [T,H] bf16, or E4M3 codes
+    x_scale: Optional[torch.Tensor]     # [T,H/128] fp32 with E4M3 codes
+
+
+def _check_layer(x, gate_up_proj, down_proj, top_k_index, top_k_weights):
+    """Shape and dtype checks of the layer's tensors (the operators check the rest)."""
+    T, H = x.shape
+    E, F2, _ = gate_up_proj.shape
+    if tuple(gate_up_proj.shape) != (E, F2, H) or tuple(down_proj.shape) != (E, H, F2 // 2) or F2 % 256 or H % 128:
+        raise ValueError("shape mismatch: x %s gate_up %s down %s (H and F multiples of 128)" % (
+            tuple(x.shape), tuple(gate_up_proj.shape), tuple(down_proj.shape)))
+    if top_k_index.dim() != 2 or top_k_index.shape[0] != T or top_k_weights.shape != top_k_index.shape:
+        raise ValueError("top_k_index / top_k_weights must be [T, K]")
+    if top_k_index.dtype != torch.int32 or top_k_weights.dtype != torch.float32:
+        raise TypeError("top_k_index must be int32 and top_k_weights float32")
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bf16")
+    for t in (x, gate_up_proj, down_proj, top_k_index, top_k_weights):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous CUDA tensors")
+
+
+def experts_forward(x, gate_up_proj, down_proj, top_k_index, top_k_weights, residual=None, keep_x="bf16",
+                    workspace=None):
+    """out [T,H] bf16 of the layer and what the backward pass needs: (out, ExpertsSaved).
+
+    x [T,H], gate_up_proj [E,2F,H], down_proj [E,H,F] bf16, top_k_index [T,K] int32, top_k_weights [T,K] fp32,
+    residual [T,H] bf16 or None (added to the sum).  keep_x: "bf16" keeps x itself (not a copy: leave it as it
+    is until the backward pass), "e4m3" an 8-bit copy.  workspace: a zeroed 8 KiB header for the products'
+    status word (moe_workspace_status); one is allocated when None."""
+    _check_layer(x, gate_up_proj, down_proj, top_k_index, top_k_weights)
+    if keep_x not in ("bf16", "e4m3"):
+        raise ValueError('keep_x must be "bf16" or "e4m3"')
+    T, K = top_k_index.shape
+    E = gate_up_proj.shape[0]
+    with torch.cuda.device(x.device):
+        _, offsets, _, inv = moe_debug_permute(top_k_index, E)
+        inv = inv.view(T, K)
+        xp, p = moe_permute_rows(x, inv, top_k_weights)
+        gu = moe_grouped_mm(xp, offsets, gate_up_proj, workspace=workspace)
+        del xp
+        h, codes, scale = moe_swiglu_checkpoint(gu, p, n_rows=offsets[E:])
+        del gu
+        y = moe_grouped_mm(h, offsets, down_proj, workspace=workspace)
+        out = moe_unpermute_rows(y, inv, residual)
+        kept, kept_scale = quantize_fp8_block128(x) if keep_x == "e4m3" and T else (x, None)
+    return out, ExpertsSaved(offsets, inv, codes, scale, p, kept, kept_scale)
+
+
+def experts_backward(saved, dout, gate_up_proj, down_proj, dgate_up=None, ddown=None, workspace=None):
+    """Gradients of experts_forward: (dx [T,H] bf16, dtop_k_weights [T,K] fp32, dgate_up [E,2F,H], ddown [E,H,F]).
+
+    dout [T,H] bf16.  dgate_up / ddown: fp32 tensors to accumulate the weights' gradients into (several
+    micro-batches); bf16 tensors are allocated when None.  A residual's gradient is dout itself."""
+    H, E = gate_up_proj.shape[2], gate_up_proj.shape[0]
+    if saved.offsets.shape[0] != E + 1:
+        raise ValueError("the saved forward had %d experts, gate_up_proj has %d" % (saved.offsets.shape[0] - 1, E))
+    if tuple(dout.shape) != (saved.inv.shape[0], H) or dout.dtype != torch.bfloat16:
+        raise ValueError("dout must be [T, H] bf16")
+    for t in (dgate_up, ddown):
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError("gradients are accumulated in fp32 tensors")
+    with torch.cuda.device(dout.device):
+        offsets, inv = saved.offsets, saved.inv
+        dy = moe_permute_rows(dout, inv)
+        dh = moe_grouped_mm_dgrad(dy, offsets, down_proj, workspace=workspace)
+        dgu, h, dp = moe_swiglu_checkpoint_backward(saved.codes, saved.scale, dh, saved.row_weights,
+                                                    n_rows=offsets[E:])
+        del dh
+        ddown = moe_grouped_mm_wgrad(dy, h, offsets, base=ddown, out=ddown, workspace=workspace)
+        del dy, h
+        xp = moe_permute_rows(saved.x, inv, x_scale=saved.x_scale)
+        dgate_up = moe_grouped_mm_wgrad(dgu, xp, offsets, base=dgate_up, out=dgate_up, workspace=workspace)
+        del xp
+        dxp = moe_grouped_mm_dgrad(dgu, offsets, gate_up_proj, workspace=workspace)
+        dx, dw = moe_unpermute_rows(dxp, inv, drow_weights=dp)
+    return dx, dw, dgate_up, ddown

@@ -1,0 +1,204 @@
+"""The training operators together: the layer's forward and backward pass
+against the oracle's forward and the 64-bit formulas at the kept activations."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from _helpers import assert_matches_oracle
+from _train_ref import BF16_HALF, F32_STEP, expert_order, restore64, swiglu_backward64
+from mixture_experts_routed_expert_b200 import inputs
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def training():
+    from mixture_experts_routed_expert_b200 import training as m
+    return m
+
+
+def _layer(T, H, F, E, K, seed=0, drop=False):
+    lay = inputs.ocr2_layer(T, seed=seed, device="cpu", H=H, F=F, E=E, K=K)
+    idx = lay.idx.clone()
+    if drop:
+        idx[::3, 0] = -1
+        idx[1::4, K - 1] = E
+    return lay, idx
+
+
+SIZES = [(1, 128, 128, 4, 2), (37, 256, 384, 8, 3), (300, 384, 256, 5, 2)]
+
+
+@pytest.mark.parametrize("T,H,F,E,K", SIZES)
+@pytest.mark.parametrize("drop", [False, True])
+def test_forward_matches_the_oracle(training, cuda_dev, T, H, F, E, K, drop):
+    lay, idx = _layer(T, H, F, E, K, drop=drop)
+    args = [t.to(cuda_dev) for t in (lay.x, lay.gate_up, lay.down, idx, lay.w)]
+    out, _ = training.experts_forward(*args)
+    ref = oracle.moe_forward_bf16(inputs.bf16_bits(lay.x), inputs.bf16_bits(lay.gate_up),
+                                  inputs.bf16_bits(lay.down), inputs.np32(idx), inputs.np32(lay.w))
+    assert_matches_oracle(out, ref, "forward")
+    res = inputs.residual_bf16(T, H)
+    with_res, _ = training.experts_forward(*args, residual=res.to(cuda_dev))
+    r = oracle.bf16_to_f64(ref) + res.double().numpy()
+    assert np.linalg.norm(with_res.double().cpu().numpy() - r) <= 5e-3 * np.linalg.norm(r)
+
+
+def _backward64(saved, lay, idx, dout, E):
+    """The formulas in 64 bits at the kept activations, each with a bound on
+    its error: a rounding to bf16 adds half a step of the value, a product
+    carries its inputs' bounds through the absolute weights and adds its own
+    fp32 sum's."""
+    T, K = idx.shape
+    off, inv = expert_order(idx, E)
+    n = int(off[-1])
+    gu = restore64(saved.codes.cpu()[:n], saved.scale.cpu()[:n])
+    F = gu.shape[1] // 2
+    x = lay.x.double() if saved.x_scale is None else \
+        restore64(saved.x.cpu(), saved.x_scale.cpu()).to(BF).double()
+    rows = torch.empty(n, dtype=torch.int64)
+    p = torch.empty(n)
+    for t in range(T):
+        for k in range(K):
+            if inv[t, k] >= 0:
+                rows[inv[t, k]], p[inv[t, k]] = t, lay.w[t, k]
+    dy, xp = dout.double()[rows], x[rows]
+    W1, W2 = lay.gate_up.double(), lay.down.double()
+    eid = torch.repeat_interleave(torch.arange(E), (off[1:] - off[:-1]).long())
+    H = dy.shape[1]
+
+    def mm(a, ea, w, terms):
+        y = torch.empty(n, w.shape[2], dtype=torch.float64)
+        m = torch.empty_like(y)
+        for e in range(E):
+            s = eid == e
+            y[s], m[s] = a[s] @ w[e], (ea[s] + (terms + 2) * F32_STEP * a[s].abs()) @ w[e].abs()
+        return y, m + BF16_HALF * (y.abs() + m)
+
+    dh, e_dh = mm(dy, torch.zeros_like(dy), W2, H)
+    dgu, h, dp = swiglu_backward64(gu, dh, p)
+    # |dgu| / |dh| is the factor of each gradient: evaluate the formula at |dh| = its bound
+    f_dgu, _, _ = swiglu_backward64(gu, e_dh, p)
+    g, u = gu.chunk(2, 1)
+    au = (g * torch.sigmoid(g) * u).abs()
+    arith = 2.0 ** -18 * swiglu_backward64(gu.abs(), dh.abs(), p)[0]
+    e_dgu = f_dgu.abs() + arith + BF16_HALF * dgu.abs()
+    e_h = (BF16_HALF + 2.0 ** -18) * h.abs()
+    e_dp = (e_dh * au).sum(1) + (2.0 ** -18 + F * F32_STEP) * (dh.abs() * au).sum(1)
+    ddown = torch.zeros(E, H, F, dtype=torch.float64)
+    dgate = torch.zeros(E, 2 * F, H, dtype=torch.float64)
+    e_ddown, e_dgate = torch.zeros_like(ddown), torch.zeros_like(dgate)
+    for e in range(E):
+        s = eid == e
+        m = int(s.sum())
+        ddown[e] = dy[s].t() @ h[s]
+        e_ddown[e] = dy[s].abs().t() @ (e_h[s] + (m + 2) * F32_STEP * h[s].abs())
+        dgate[e] = dgu[s].t() @ xp[s]
+        e_dgate[e] = (e_dgu[s] + (m + 2) * F32_STEP * dgu[s].abs()).t() @ xp[s].abs()
+    dxp, e_dxp = mm(dgu, e_dgu, W1, 2 * F)
+    dx, e_dx = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
+    dw, e_dw = torch.zeros(T, K, dtype=torch.float64), torch.zeros(T, K, dtype=torch.float64)
+    for t in range(T):
+        for k in range(K):
+            q = int(inv[t, k])
+            if q >= 0:
+                dx[t] += dxp[q]
+                e_dx[t] += e_dxp[q] + K * F32_STEP * dxp[q].abs()
+                dw[t, k], e_dw[t, k] = dp[q], e_dp[q]
+    e_dx += BF16_HALF * (dx.abs() + e_dx)
+    return (dx, e_dx), (dw, e_dw), (dgate, e_dgate), (ddown, e_ddown)
+
+
+def _check(got, want, what, rounded=False):
+    ref, tol = want
+    if rounded:
+        tol = tol + BF16_HALF * (ref.abs() + tol)
+    off = (got.double().cpu() - ref).abs()
+    assert torch.isfinite(got).all(), what
+    assert not (off > tol + 1e-30).any(), "%s: worst %.2f of the tolerance" % (
+        what, float((off / (tol + 1e-30)).max()))
+
+
+@pytest.mark.parametrize("T,H,F,E,K", SIZES)
+@pytest.mark.parametrize("keep_x", ["bf16", "e4m3"])
+def test_backward_matches_the_formulas(training, cuda_dev, T, H, F, E, K, keep_x):
+    lay, idx = _layer(T, H, F, E, K, seed=1, drop=T > 1)
+    dout = torch.randn(T, H, generator=torch.Generator().manual_seed(3)).to(BF)
+    x, gu, dn, i, w, do = (t.to(cuda_dev) for t in (lay.x, lay.gate_up, lay.down, idx, lay.w, dout))
+    _, saved = training.experts_forward(x, gu, dn, i, w, keep_x=keep_x)
+    got = training.experts_backward(saved, do, gu, dn)
+    want = _backward64(saved, lay, idx, dout, E)
+    for g, r, what, rounded in zip(got, want, ("dx", "dtop_k_weights", "dgate_up", "ddown"),
+                                   (False, False, True, True)):
+        _check(g, r, what, rounded)
+    # accumulated into fp32: the second micro-batch adds to the first
+    a1, a2 = torch.zeros(E, 2 * F, H, device=cuda_dev), torch.zeros(E, H, F, device=cuda_dev)
+    for _ in range(2):
+        _, _, r1, r2 = training.experts_backward(saved, do, gu, dn, dgate_up=a1, ddown=a2)
+    assert r1 is a1 and r2 is a2
+    for a, (ref, tol), what in ((a1, want[2], "dgate_up"), (a2, want[3], "ddown")):
+        _check(a, (2 * ref, 2 * tol + F32_STEP * 2 * (ref.abs() + tol)), what + " of two")
+
+
+def test_no_tokens(training, cuda_dev):
+    gu, dn = torch.zeros(4, 256, 128, dtype=BF, device=cuda_dev), torch.zeros(4, 128, 128, dtype=BF, device=cuda_dev)
+    x = torch.empty(0, 128, dtype=BF, device=cuda_dev)
+    idx, w = torch.empty(0, 2, dtype=torch.int32, device=cuda_dev), torch.empty(0, 2, device=cuda_dev)
+    for keep in ("bf16", "e4m3"):
+        out, saved = training.experts_forward(x, gu, dn, idx, w, keep_x=keep)
+        assert out.shape == (0, 128)
+        dx, dw, dgu, ddn = training.experts_backward(saved, out, gu, dn)
+        assert dx.shape == (0, 128) and dw.shape == (0, 2) and (dgu == 0).all() and (ddn == 0).all()
+
+
+def test_step_in_a_graph(training, cuda_dev):
+    """A captured forward and backward replays on new inputs with the bits of
+    the eager calls; no product ran into its time limit."""
+    T, H, F, E, K = 64, 256, 256, 6, 2
+    lay, idx = _layer(T, H, F, E, K, seed=4)
+    x, gu, dn, i, w = (t.to(cuda_dev) for t in (lay.x, lay.gate_up, lay.down, idx, lay.w))
+    do = torch.randn(T, H, generator=torch.Generator().manual_seed(5)).to(BF).to(cuda_dev)
+    ws = torch.zeros(8192, dtype=torch.uint8, device=cuda_dev)
+
+    def step():
+        out, saved = training.experts_forward(x, gu, dn, i, w, workspace=ws)
+        return (out,) + training.experts_backward(saved, do, gu, dn, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        caught = step()
+    lay2, idx2 = _layer(T, H, F, E, K, seed=6)
+    x.copy_(lay2.x)
+    i.copy_(idx2)
+    w.copy_(lay2.w)
+    g.replay()
+    torch.cuda.synchronize()
+    eager = step()
+    torch.cuda.synchronize()
+    for a, b in zip(caught, eager):
+        assert torch.equal(a, b)
+    moe = __import__("mixture_experts_routed_expert_b200")
+    assert moe.moe_workspace_status(ws) == 0
+
+
+def test_refusals(training, cuda_dev):
+    T, H, F, E, K = 4, 128, 128, 4, 2
+    lay, idx = _layer(T, H, F, E, K)
+    x, gu, dn, i, w = (t.to(cuda_dev) for t in (lay.x, lay.gate_up, lay.down, idx, lay.w))
+    out, saved = training.experts_forward(x, gu, dn, i, w)
+    for bad in (lambda: training.experts_forward(x, gu, dn, i, w, keep_x="fp8"),
+                lambda: training.experts_forward(x, gu, dn[:, :64], i, w),
+                lambda: training.experts_forward(x.cpu(), gu, dn, i, w),
+                lambda: training.experts_backward(saved, out[:2], gu, dn),
+                lambda: training.experts_backward(saved, out, gu[:2], dn[:2])):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: training.experts_forward(x, gu, dn, i.long(), w),
+                lambda: training.experts_backward(saved, out, gu, dn, ddown=torch.zeros_like(dn))):
+        with pytest.raises(TypeError):
+            bad()
