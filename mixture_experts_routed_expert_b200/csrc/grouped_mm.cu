@@ -49,6 +49,7 @@ constexpr int kTM = 256;                       // A-side width of a pair's tile
 constexpr int kABytes = kBM * 128;
 constexpr int kOutStage = 2 * 32 * kBM * 2;    // per epilogue set 32 rows x 128 columns of bf16
 constexpr int kChunkBytes = 64 * 128;          // MN-major: 64 elements x 64 reduction rows
+constexpr int kBand = 8;                       // row tiles of a band
 constexpr int kRaggedDelay = 1;                // k-blocks multiplied before a ragged one that was loaded first
 
 // BN: B-side width of a pair's tile; each CTA holds half of B.
@@ -237,8 +238,12 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
         }
         t.e = lo;
         const int nt = s_tiles[lo + 1] - s_tiles[lo];
+        // row tiles fastest (they share a weight tile), in bands of kBand
+        // that go over all columns: a band's rows stay in L2
         const int local = w - s_tiles[lo] * MT;
-        const int m = local / nt, n = local - m * nt;
+        const int band = local / (kBand * MT);
+        const int in_band = local - band * (kBand * MT), width = min(kBand, nt - band * kBand);
+        const int m = in_band / width, n = band * kBand + in_band - m * width;
         const int n_e = s_end[lo] - s_beg[lo];
         const int rpt = min(BN, ((n_e + nt - 1) / nt + 15) & ~15);
         t.m0 = m * kTM;
