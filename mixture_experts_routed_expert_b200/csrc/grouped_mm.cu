@@ -47,7 +47,7 @@ enum Op : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 constexpr int kBK = 64;                        // reduction elements per stage = one 128-byte swizzle row
 constexpr int kTM = 256;                       // A-side width of a pair's tile
 constexpr int kABytes = kBM * 128;
-constexpr int kOutStage = 2 * 32 * kBM * 2;    // per epilogue set 32 rows x 128 columns of bf16
+constexpr int kOutStage = 8 * 32 * 64;         // per epilogue warp 32 rows x 32 columns of bf16
 constexpr int kChunkBytes = 64 * 128;          // MN-major: 64 elements x 64 reduction rows
 constexpr int kBand = 8;                       // row tiles of a band
 constexpr int kRaggedDelay = 1;                // k-blocks multiplied before a ragged one that was loaded first
@@ -55,7 +55,10 @@ constexpr int kRaggedDelay = 1;                // k-blocks multiplied before a r
 // BN: B-side width of a pair's tile; each CTA holds half of B.
 template <int OP, bool OUT_BF16, int BN>
 struct MmCfg {
-    static constexpr int kStages = BN == 256 ? 6 : 9;
+    // The weight gradient, which also streams its output (and base) through
+    // L2, is faster with less in flight: N=7168 C=2048, fp32 with base, 4 / 5 /
+    // 6 stages 899 / 892 / 951 us; forward of 12288 rows, 5 / 6 stages 72 / 69 us.
+    static constexpr int kStages = OP == kWgrad ? 5 : BN == 256 ? 6 : 9;
     static constexpr int kBBytes = BN / 2 * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kRingBytes = kStages * kStageBytes;
@@ -133,22 +136,6 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t saddr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
     return v;
-}
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-// named_barrier that also says whether every thread brought a true `v`.
-__device__ __forceinline__ bool named_barrier_all(int id, int threads, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(id), "r"(threads)
-        : "memory");
-    return r != 0;
 }
 // True in one lane of a converged warp (the same on every call).
 __device__ __forceinline__ bool elect_one() {
@@ -527,7 +514,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
         // ------------------------------------------------ epilogue --------
         const int eg = warp & 3;                // TMEM lanes [32*eg, 32*eg+32)
         const int set = (warp - 2) >> 2;        // which 32-column chunks
-        const uint32_t stg = smem_u32(s_out) + set * (32 * kBM * 2);   // [32 rows][16 units of 8 columns]
+        const uint32_t stg = smem_u32(s_out) + (warp - 2) * (32 * 64);   // [32 rows][64 bytes]
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int w = pair; w < total; w += pairs) {
@@ -556,8 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
             };
             read_base(set * 32);
             if (!none) {
-                // the set's warps agree, so that none waits for another below
-                if (!named_barrier_all(1 + set, 128, mbar_wait(&tfull[acc], acc_phase, abort_flag))) {
+                if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) {
                     *abort_flag = 1;
                     atomicOr(args.status, DEV_TIMEOUT);
                     break;
@@ -581,16 +567,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                 } else if (OUT_BF16) {
                     tmem_ld_16x32(tb + c0, g);
                     tmem_ld_16x32(tb + c0 + (16u << 16), g + 16);
-                    tmem_ld_wait();
                 } else {
                     tmem_ld32(tb + c0, g);
-                    tmem_ld_wait();
                 }
+                tmem_ld_wait_regs16(g);
+                tmem_ld_wait_regs16(g + 16);
                 if (c0 + 32 * C::kSets >= t.nrows) release();
                 if (OUT_BF16) {
                     // g[h*16 + i*4 + o*2 + {0,1}]: TMEM lane h*16 + o*8 + lane/4, columns 8i + 2(lane%4) + {0,1}.
-                    // Transposed 8x8 blocks to shared memory: row = accumulator column, 16-byte
-                    // units of 8 lanes, unit index xor row % 8 (no bank conflicts either way).
+                    // Transposed 8x8 blocks to this warp's buffer: row = accumulator column, four
+                    // 16-byte units of 8 lanes, unit index xor (row / 2) % 4 (no bank conflicts
+                    // either way).  A buffer shared by the four quarters would make the rows
+                    // 256 bytes long, but its two barriers a chunk cost more than all the rest
+                    // (64 experts x 64 rows, N=7168, C=2048: 417 us, so 0.2 of the chunk's 0.5 us).
                     const int q = lane >> 3, jj = lane & 7;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -600,19 +589,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                             const uint32_t *v = g + (o >> 1) * 16 + i * 4 + (o & 1) * 2;
                             p[o] = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
                         }
-                        stmatrix4_trans(stg + (8 * i + jj) * (kBM * 2) + (((eg * 4 + q) ^ jj) << 4), p);
+                        stmatrix4_trans(stg + (8 * i + jj) * 64 + ((q ^ ((jj >> 1) & 3)) << 4), p);
                     }
-                    named_barrier(1 + set, 128);
-                    // 8 rows per warp, 256 contiguous bytes each
+                    __syncwarp();
+                    // 8 rows x 64 bytes an instruction
+                    const int u = lane & 3, mu = mc + eg * 32 + u * 8;
+                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(args.out) + (orow + c0 + (lane >> 2)) * args.M + mu;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = eg * 8 + i * 2 + (lane >> 4), u = lane & 15;
-                        const uint4 v = ld_shared16(stg + r * (kBM * 2) + ((u ^ (r & 7)) << 4));
-                        if (c0 + r < t.nrows && mc + u * 8 < args.M)
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(args.out) +
-                                                       (orow + c0 + r) * args.M + mc + u * 8) = v;
+                    for (int i = 0; i < 4; ++i, o += (size_t)8 * args.M) {
+                        const int r = (lane >> 2) + 8 * i;
+                        const uint4 v = ld_shared16(stg + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+                        if (c0 + r < t.nrows && mu < args.M) *reinterpret_cast<uint4 *>(o) = v;
                     }
-                    named_barrier(1 + set, 128);
+                    __syncwarp();
                 } else {
                     if (OP == kWgrad && args.base) {
 #pragma unroll
