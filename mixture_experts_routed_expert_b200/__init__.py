@@ -458,18 +458,21 @@ def _enqueue(name, stream, *args):
         else:
             at.append(a.data_ptr())
     fn = getattr(_lib(), name)
-    if stream is None and dev == torch._C._cuda_getDevice():
-        rc = fn(*at, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        if stream is not None:
-            if stream.device_index != dev:
-                raise ValueError("%s: the stream belongs to device %d, the tensors to %d" % (
-                    name, stream.device_index, dev))
+    raw = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError("%s: the stream belongs to device %d, the tensors to %d" % (
+                name, stream.device_index, dev))
+        if stream.cuda_stream != raw:
+            raw = stream.cuda_stream
             for a in args:
                 if isinstance(a, torch.Tensor):
                     a.record_stream(stream)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*at, raw)
+    else:
         with torch.cuda.device(dev):
-            rc = fn(*at, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+            rc = fn(*at, raw)
     if rc:
         _check(rc, name)
 

@@ -113,9 +113,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // 16 TMEM lanes x 32 columns: register 4i + 2o + c of a thread holds lane
 // 8o + lane/4, column 8i + 2(lane%4) + c.
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t *r) {
@@ -292,6 +291,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
         prefetch_tmap(&tmB);
     }
     if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * BN);
+    __syncwarp();
+    cluster_arrive();                          // this CTA's barriers and TMEM are ready
     pdl_wait();
     // Row ranges of the experts, clamped into the matrices whatever the
     // offsets hold, and the prefix sum of their row tiles: each thread sums a
@@ -324,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
     tc_fence_before();
     __syncthreads();
     __syncwarp();
-    cluster_sync();                            // both CTAs' barriers and TMEM are ready
+    cluster_wait();                            // and the other CTA's
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int MT = (args.M + kTM - 1) / kTM;
@@ -629,7 +630,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
     tc_fence_before();
     __syncthreads();
     __syncwarp();
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 2 * BN);

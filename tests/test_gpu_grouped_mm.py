@@ -201,3 +201,89 @@ def test_same_bits_graph_and_streams(moe, cuda_dev):
     for a, b in zip(caught, again):
         assert torch.equal(a, b)
     assert moe.moe_workspace_status(ws) == 0
+
+
+def test_rows_without_experts(moe, cuda_dev):
+    """Rows are there but every expert is empty: weight gradients are zeros or
+    the base, row outputs stay as they were."""
+    o = torch.full((4,), 33, dtype=torch.int32, device=cuda_dev)
+    x = torch.full((50, 72), float("nan"), dtype=BF, device=cuda_dev)
+    dy = torch.full((50, 40), float("inf"), dtype=BF, device=cuda_dev)
+    w = torch.zeros(3, 40, 72, dtype=BF, device=cuda_dev)
+    base = torch.randn(3, 40, 72, device=cuda_dev)
+    for dt in (BF, F32):
+        dw = torch.full((3, 40, 72), 5.0, dtype=dt, device=cuda_dev)
+        assert (moe.moe_grouped_mm_wgrad(dy, x, o, out=dw) == 0).all()
+        y = torch.full((50, 40), 5.0, dtype=dt, device=cuda_dev)
+        dx = torch.full((50, 72), 5.0, dtype=dt, device=cuda_dev)
+        assert (moe.moe_grouped_mm(x, o, w, out=y) == 5).all()
+        assert (moe.moe_grouped_mm_dgrad(dy, o, w, out=dx) == 5).all()
+    assert torch.equal(moe.moe_grouped_mm_wgrad(dy, x, o, base=base), base)
+    copy = base.clone()
+    assert torch.equal(moe.moe_grouped_mm_wgrad(dy, x, o, base=copy, out=copy), base)
+
+
+@pytest.mark.parametrize("rows", [40, 3000])
+def test_views_of_larger_buffers(moe, cuda_dev, rows):
+    """Contiguous views that start 16 bytes into an allocation, as slices of a
+    pool do: the smallest alignment the entry points take."""
+    def at16(t):
+        b = torch.empty(t.numel() + 64, dtype=t.dtype, device=cuda_dev)
+        k = 16 // t.element_size()
+        v = b[k:k + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+    off, x, dy, w = _inputs([rows // 4, rows - rows // 4], 136, 200, seed=11)
+    o, xd, dd, wd = off.to(cuda_dev), at16(x), at16(dy), at16(w)
+    assert xd.data_ptr() % 32 == 16
+    y, dx = at16(torch.zeros(rows, 136, dtype=BF)), at16(torch.zeros(rows, 200, dtype=BF))
+    dw = at16(torch.zeros(2, 136, 200))
+    check_sum(moe.moe_grouped_mm(xd, o, wd, out=y), *mm64(x, off, w, False), 200)
+    check_sum(moe.moe_grouped_mm_dgrad(dd, o, wd, out=dx), *mm64(dy, off, w, True), 136)
+    check_sum(moe.moe_grouped_mm_wgrad(dd, xd, o, base=dw, out=dw), *wgrad64(dy, x, off), rows)
+
+
+def test_outputs_past_32_bits(moe, cuda_dev):
+    """Outputs whose element offsets pass 2^31: the last rows are right and lie
+    at the end."""
+    rows, N, C = 33000, 65536, 8
+    g = torch.Generator(device=cuda_dev).manual_seed(12)
+    x = torch.randn(rows, C, generator=g, device=cuda_dev).to(BF)
+    w = (torch.randn(2, N, C, generator=g, device=cuda_dev) * 0.1).to(BF)
+    off = offsets_of([32900, 100])
+    y = moe.moe_grouped_mm(x, off.to(cuda_dev), w)
+    for a, e in ((0, 0), (32800, 0), (32900, 1), (32990, 1)):
+        r = slice(a, a + 10)
+        ref, mag = x[r].double() @ w[e].double().t(), x[r].double().abs() @ w[e].double().abs().t()
+        check_sum(y[r], ref.cpu(), mag.cpu(), C, "rows from %d" % a)
+    del y
+    # weight gradient [E, N, C] past 2^31 elements: many experts, one row each but the last
+    E, N, C = 1024, 2048, 1032
+    off = offsets_of([1] * (E - 1) + [40])
+    x = torch.randn(E + 39, C, generator=g, device=cuda_dev).to(BF)
+    dy = torch.randn(E + 39, N, generator=g, device=cuda_dev).to(BF)
+    dw = moe.moe_grouped_mm_wgrad(dy, x, off.to(cuda_dev))
+    for e, a, b in ((0, 0, 1), (E - 2, E - 2, E - 1), (E - 1, E - 1, E + 39)):
+        ref, mag = dy[a:b].double().t() @ x[a:b].double(), dy[a:b].double().abs().t() @ x[a:b].double().abs()
+        check_sum(dw[e], ref.cpu(), mag.cpu(), b - a, "expert %d" % e)
+
+
+def test_another_stream_keeps_its_tensors(moe, cuda_dev):
+    """Tensors made on the current stream and dropped right after a call on
+    another one stay whole until that call has read them."""
+    off, x, dy, w = _inputs([300, 212], 512, 512, seed=13)
+    o, wd = off.to(cuda_dev), w.to(cuda_dev)
+    side = torch.cuda.Stream()
+    want = moe.moe_grouped_mm(x.to(cuda_dev), o, wd)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        xd = x.to(cuda_dev)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+        outs.append(moe.moe_grouped_mm(xd, o, wd, stream=side))
+        del xd
+        torch.full((512, 512), float("nan"), dtype=BF, device=cuda_dev)      # takes freed memory at once
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in outs)

@@ -121,3 +121,16 @@ def test_empty(moe, cuda_dev):
     none = torch.empty(0, 2, dtype=torch.int32, device=cuda_dev)
     assert moe.moe_permute_rows(torch.empty(0, 64, dtype=BF, device=cuda_dev), none).shape == (0, 64)
     assert moe.moe_unpermute_rows(torch.ones(3, 64, dtype=BF, device=cuda_dev), none).shape == (0, 64)
+
+
+def test_offsets_past_32_bits(moe, cuda_dev):
+    """More than 2^31 elements on the expert-order side."""
+    T, K, H = 9000, 16, 16384
+    g = torch.Generator(device=cuda_dev).manual_seed(3)
+    inv = torch.randperm(T * K, generator=g, device=cuda_dev).to(torch.int32).view(T, K)
+    x = torch.randn(T, H, generator=g, device=cuda_dev).to(BF)
+    rows = moe.moe_permute_rows(x, inv)
+    for t in (0, 4500, T - 1):
+        assert torch.equal(rows[inv[t].long()], x[t].expand(K, H))
+    out = moe.moe_unpermute_rows(rows, inv)
+    assert torch.equal(out, (x.float() * K).to(BF))         # 16 equal terms: every partial sum is exact in fp32

@@ -169,3 +169,27 @@ def test_graph_and_stream(moe, cuda_dev):
     torch.cuda.synchronize()
     for a, b in zip(caught, other):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(moe, cuda_dev):
+    rows, F = 70000, 16384                                   # gate_up: 2.3e9 elements
+    last = 64
+    gu = torch.zeros(rows, 2 * F, dtype=BF, device=cuda_dev)
+    tail, g = _gate_up(last, F, 7)
+    gu[-last:] = tail.to(cuda_dev)
+    h, codes, scale = moe.moe_swiglu_checkpoint(gu)
+    del gu
+    q, s = quantize64(tail)
+    assert torch.equal(scale[-last:].cpu().double(), s)
+    assert torch.equal(codes[-last:].cpu().view(torch.float8_e4m3fn).double(), q)
+    ref = swiglu64(tail)
+    _near(h[-last:], ref, (BF16_HALF + ARITH) * ref.abs(), "h")
+    assert (h[:1000] == 0).all() and (codes[:1000] == 0).all() and (scale[:1000] == 1).all()
+    dh = torch.zeros(rows, F, dtype=BF, device=cuda_dev)
+    d = torch.randn(last, F, generator=g).to(BF)
+    dh[-last:] = d.to(cuda_dev)
+    del h
+    dgu, hb, dp = moe.moe_swiglu_checkpoint_backward(codes, scale, dh)
+    _, rh, _ = swiglu_backward64(restore64(codes[-last:].cpu(), scale[-last:].cpu()), d)
+    _near(hb[-last:], rh, (BF16_HALF + ARITH) * rh.abs(), "h")
+    assert (dgu[:1000] == 0).all() and (dp[:-last] == 0).all() and (dgu[-last:] != 0).float().mean() > 0.9
