@@ -29,9 +29,10 @@
 // Persistent: one CTA per SM, the pairs walk the tile list, which every CTA
 // derives from the offsets on the device.  Warp roles: 0 TMA producer of the
 // CTA's own operands (both CTAs' copies complete on the leading CTA's
-// barrier); 1 in the leading CTA MMA issue for the pair; 2 on epilogue (two
-// sets of four warps, one warp per TMEM lane quarter, each set every other 32
-// accumulator columns); the last (weight gradient) zeroes the ragged end.
+// barrier); 1 in the leading CTA MMA issue for the pair; 2 on epilogue (two or
+// four sets of four warps, one warp per TMEM lane quarter, the sets taking
+// turns at 32 accumulator columns); the last (weight gradient) zeroes the
+// ragged end.
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -50,6 +51,12 @@ constexpr int kABytes = kBM * 128;
 constexpr int kOutStage = 8 * 32 * 64;         // per epilogue warp 32 rows x 32 columns of bf16
 constexpr int kChunkBytes = 64 * 128;          // MN-major: 64 elements x 64 reduction rows
 constexpr int kBand = 8;                       // row tiles of a band
+// k-blocks that the tensor cores sum for an fp32 output before the epilogue
+// takes the partial sum into its registers.  Their accumulation truncates: a
+// sum of K products came out 9.5e-10 K too small, relatively (K = 512: 4.8e-7,
+// K = 7168: 7.9e-6, against 2.2e-7 for fp32 products rounded one by one).  512
+// at a time keep every K under 1e-6.  A bf16 output's half step (2e-3) hides it.
+constexpr int kPartBlocks = 8;
 constexpr int kRaggedDelay = 1;                // k-blocks multiplied before a ragged one that was loaded first
 
 // BN: B-side width of a pair's tile; each CTA holds half of B.
@@ -62,7 +69,9 @@ struct MmCfg {
     static constexpr int kBBytes = BN / 2 * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kRingBytes = kStages * kStageBytes;
-    static constexpr int kEpiWarps = 8;
+    // fp32 outputs sum in registers: 32 columns x BN / kSets rows a warp; with 8 warps the
+    // weight gradient's 352 threads would have 168 registers each, and spill
+    static constexpr int kEpiWarps = OP == kWgrad && !OUT_BF16 ? 16 : 8;
     static constexpr int kSets = kEpiWarps / 4;
     static constexpr int kThreads = 64 + 32 * kEpiWarps + (OP == kWgrad ? 32 : 0);
     static_assert(kRaggedDelay + 2 <= kStages && (OP != kWgrad || BN / 2 % 64 == 0), "");
@@ -423,12 +432,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                 const uint32_t idesc = idesc_bf16(kTM, (t.nrows + 15) & ~15) | kMajor;
                 if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d = tmem_base + acc * BN;
+                uint32_t d = tmem_base + acc * BN;
                 const bool ends_ragged = ragged_end<OP>(t);
                 const int delay = ends_ragged ? min(KB - 1, kRaggedDelay) : 0;
                 int stage = stage0;
                 uint32_t phase = phase0;
                 for (int i = 0; i < KB; ++i) {
+                    if (!OUT_BF16 && i > 0 && i % kPartBlocks == 0) {    // the next partial sum
+                        if (issuer) mma_commit_pair(&tfull[acc]);
+                        __syncwarp();
+                        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                        if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        d = tmem_base + acc * BN;
+                    }
+                    const bool first = OUT_BF16 ? i == 0 : i % kPartBlocks == 0;
                     // the ragged k-block sits in the first stage; its turn comes after `delay` others
                     const bool ragged = ends_ragged && i == delay;
                     if (ends_ragged && i == 0 && !ragged && ++stage == C::kStages) { stage = 0; phase ^= 1; }
@@ -444,10 +462,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                         if (steps == kBK / 16) {
 #pragma unroll
                             for (int k = 0; k < kBK / 16; ++k)
-                                mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (i | k) != 0);
+                                mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, !first || k != 0);
                         } else {
                             for (int k = 0; k < steps; ++k)
-                                mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, (i | k) != 0);
+                                mma_bf16_pair(d, da + kStepA * k, db + kStepB * k, idesc, !first || k != 0);
                         }
                         mma_commit_pair(&empty[at]);
                     }
@@ -525,24 +543,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
             if (none && args.base == args.out && args.base != nullptr) continue;
             const size_t orow = OP == kWgrad ? (size_t)t.e * args.N + t.row0 : (size_t)t.row0;
             const int mc = t.m0 + rank * kBM;   // first output column of this CTA
-            // fp32: first output element of this lane in a chunk, and the base of
-            // the chunk to come (read a chunk ahead of its use, before any store
-            // of the chunk: base may be out itself)
-            const bool mine = mc + eg * 32 + lane < args.M;
-            const size_t at0 = orow * args.M + mc + eg * 32 + lane;
-            float b[32];
-            auto read_base = [&](int c0) {
-                if (OP != kWgrad || OUT_BF16 || args.base == nullptr || !mine) return;
-                const float *p = args.base + at0 + (size_t)c0 * args.M;
-                if (c0 + 32 <= t.nrows) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = *p;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j, p += args.M) b[j] = c0 + j < t.nrows ? *p : 0.f;
-                }
+            const uint32_t lanes = tmem_base + ((uint32_t)(eg * 32) << 16);
+            // the accumulator is free again once this warp's last columns are in registers
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_leader(&tempty[acc]);
             };
-            read_base(set * 32);
+            if (!OUT_BF16) {
+                // This lane's output column, NI times 32 rows of it in registers: the
+                // base to begin with (asked for before the product is there, and
+                // wholly read before any store: it may be out itself), plus each
+                // partial sum in turn.
+                constexpr int NI = BN / (32 * C::kSets);
+                float sum[NI][32];
+                const bool mine = mc + eg * 32 + lane < args.M;
+                const size_t at0 = orow * args.M + mc + eg * 32 + lane;
+                const bool based = OP == kWgrad && args.base != nullptr && mine;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int c0 = (set + C::kSets * i) * 32;
+                    const float *p = args.base + at0 + (size_t)c0 * args.M;
+                    if (based && c0 + 32 <= t.nrows) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, p += args.M) sum[i][j] = *p;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, p += args.M) sum[i][j] = based && c0 + j < t.nrows ? *p : 0.f;
+                    }
+                }
+                const int parts = ((t.red + kBK - 1) / kBK + kPartBlocks - 1) / kPartBlocks;
+                bool ok = true;
+                for (int part = 0; part < parts; ++part) {
+                    ok = mbar_wait(&tfull[acc], acc_phase, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int c0 = (set + C::kSets * i) * 32;
+                        if (c0 >= t.nrows) break;
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t g[16];
+                            tmem_ld16(lanes + acc * BN + c0 + h, g);
+                            tmem_ld_wait_regs16(g);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[i][h + j] += __uint_as_float(g[j]);
+                        }
+                    }
+                    release();
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                }
+                if (!ok) {
+                    *abort_flag = 1;
+                    atomicOr(args.status, DEV_TIMEOUT);
+                    break;
+                }
+                // one check per 32 rows: a compare, a branch and a 64-bit product a
+                // store made 600 instructions of them and held the stores at 3 TB/s
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int c0 = (set + C::kSets * i) * 32;
+                        float *o = static_cast<float *>(args.out) + at0 + (size_t)c0 * args.M;
+                        if (c0 + 32 <= t.nrows) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j, o += args.M) *o = sum[i][j];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j, o += args.M)
+                                if (c0 + j < t.nrows) *o = sum[i][j];
+                        }
+                    }
+                }
+                continue;
+            }
             if (!none) {
                 if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) {
                     *abort_flag = 1;
@@ -550,77 +625,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                     break;
                 }
                 tc_fence_after();
+                if (set * 32 >= t.nrows) release();
             }
-            const uint32_t tb = tmem_base + ((uint32_t)(eg * 32) << 16) + acc * BN;
-            // the accumulator is free again once this warp's last chunk is in registers
-            auto release = [&]() {
-                if (none) return;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_leader(&tempty[acc]);
-            };
-            if (set * 32 >= t.nrows) release();
             for (int c0 = set * 32; c0 < t.nrows; c0 += 32 * C::kSets) {
                 uint32_t g[32];
                 if (none) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) g[j] = 0;
-                } else if (OUT_BF16) {
-                    tmem_ld_16x32(tb + c0, g);
-                    tmem_ld_16x32(tb + c0 + (16u << 16), g + 16);
                 } else {
-                    tmem_ld32(tb + c0, g);
+                    tmem_ld_16x32(lanes + acc * BN + c0, g);
+                    tmem_ld_16x32(lanes + acc * BN + c0 + (16u << 16), g + 16);
+                    tmem_ld_wait_regs16(g);
+                    tmem_ld_wait_regs16(g + 16);
+                    if (c0 + 32 * C::kSets >= t.nrows) release();
                 }
-                tmem_ld_wait_regs16(g);
-                tmem_ld_wait_regs16(g + 16);
-                if (c0 + 32 * C::kSets >= t.nrows) release();
-                if (OUT_BF16) {
-                    // g[h*16 + i*4 + o*2 + {0,1}]: TMEM lane h*16 + o*8 + lane/4, columns 8i + 2(lane%4) + {0,1}.
-                    // Transposed 8x8 blocks to this warp's buffer: row = accumulator column, four
-                    // 16-byte units of 8 lanes, unit index xor (row / 2) % 4 (no bank conflicts
-                    // either way).  A buffer shared by the four quarters would make the rows
-                    // 256 bytes long, but its two barriers a chunk cost more than all the rest
-                    // (64 experts x 64 rows, N=7168, C=2048: 417 us, so 0.2 of the chunk's 0.5 us).
-                    const int q = lane >> 3, jj = lane & 7;
+                // g[h*16 + i*4 + o*2 + {0,1}]: TMEM lane h*16 + o*8 + lane/4, columns 8i + 2(lane%4) + {0,1}.
+                // Transposed 8x8 blocks to this warp's buffer: row = accumulator column, four
+                // 16-byte units of 8 lanes, unit index xor (row / 2) % 4 (no bank conflicts
+                // either way).  A buffer shared by the four quarters would make the rows
+                // 256 bytes long, but its two barriers a chunk cost more than all the rest
+                // (64 experts x 64 rows, N=7168, C=2048: 417 us, so 0.2 of the chunk's 0.5 us).
+                const int q = lane >> 3, jj = lane & 7;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t p[4];
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t p[4];
 #pragma unroll
-                        for (int o = 0; o < 4; ++o) {
-                            const uint32_t *v = g + (o >> 1) * 16 + i * 4 + (o & 1) * 2;
-                            p[o] = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                        }
-                        stmatrix4_trans(stg + (8 * i + jj) * 64 + ((q ^ ((jj >> 1) & 3)) << 4), p);
+                    for (int o = 0; o < 4; ++o) {
+                        const uint32_t *v = g + (o >> 1) * 16 + i * 4 + (o & 1) * 2;
+                        p[o] = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
                     }
-                    __syncwarp();
-                    // 8 rows x 64 bytes an instruction
-                    const int u = lane & 3, mu = mc + eg * 32 + u * 8;
-                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(args.out) + (orow + c0 + (lane >> 2)) * args.M + mu;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i, o += (size_t)8 * args.M) {
-                        const int r = (lane >> 2) + 8 * i;
-                        const uint4 v = ld_shared16(stg + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
-                        if (c0 + r < t.nrows && mu < args.M) *reinterpret_cast<uint4 *>(o) = v;
-                    }
-                    __syncwarp();
-                } else {
-                    if (OP == kWgrad && args.base) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(__uint_as_float(g[j]) + b[j]);
-                        read_base(c0 + 32 * C::kSets);
-                    }
-                    // one check a chunk: a compare, a branch and a 64-bit product a store
-                    // made 600 instructions of a chunk and held the stores at 3 TB/s
-                    float *o = static_cast<float *>(args.out) + at0 + (size_t)c0 * args.M;
-                    if (mine && c0 + 32 <= t.nrows) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j, o += args.M) *o = __uint_as_float(g[j]);
-                    } else if (mine) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j, o += args.M)
-                            if (c0 + j < t.nrows) *o = __uint_as_float(g[j]);
-                    }
+                    stmatrix4_trans(stg + (8 * i + jj) * 64 + ((q ^ ((jj >> 1) & 3)) << 4), p);
                 }
+                __syncwarp();
+                // 8 rows x 64 bytes an instruction
+                const int u = lane & 3, mu = mc + eg * 32 + u * 8;
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(args.out) + (orow + c0 + (lane >> 2)) * args.M + mu;
+#pragma unroll
+                for (int i = 0; i < 4; ++i, o += (size_t)8 * args.M) {
+                    const int r = (lane >> 2) + 8 * i;
+                    const uint4 v = ld_shared16(stg + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+                    if (c0 + r < t.nrows && mu < args.M) *reinterpret_cast<uint4 *>(o) = v;
+                }
+                __syncwarp();
             }
             if (none) continue;
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
