@@ -404,184 +404,94 @@ def moe_debug_permute(top_k_index, E, workspace=None, stream=None):
 
 
 # ---- the training step's operators -----------------------------------------
-# Tensors may live on any device: the call is made on the tensors' device, on
-# `stream` (default: that device's current stream).  With a stream given,
-# outputs are allocated on it and the inputs are recorded as in use by it.
-# The checks are kept lean: a step makes dozens of these calls, and the small
-# ones run for a few microseconds.
+# Argument checks, outputs and the call are native (csrc/binding.cpp, built as
+# _native.so beside the library).  Tensors may live on any device: the call is
+# made on the tensors' device, on `stream` (default: that device's current
+# stream).  With a stream given, outputs are allocated on it and the inputs
+# are recorded as in use by it.
 
-_OTYPE = {torch.bfloat16: 0, torch.float32: 1}   # moe_otype_t
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-
-
-def _want(what, t, dtype, shape):
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
+_OTYPE = {None: -1, torch.bfloat16: 0, torch.float32: 1}   # moe_otype_t, -1: not asked for
+_NATIVE = None
 
 
-def _codes(what, t, shape):
-    if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
-        raise TypeError("%s must be E4M3 codes (uint8 / float8_e4m3fn), got %s" % (what, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
+def _native():
+    """The training operators' binding (loaded on the first call)."""
+    global _NATIVE
+    if _NATIVE is None:
+        path = os.path.join(_HERE, "_native.so")
+        if not os.path.exists(path):
+            raise ImportError("_native.so is not built (run __graft_entry__.build() or "
+                              "python -m mixture_experts_routed_expert_b200.build)")
+        import importlib.machinery
+        import importlib.util
+        loader = importlib.machinery.ExtensionFileLoader(__name__ + "._native", path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+        loader.exec_module(mod)
+        mod.set_check(_check)
+        _NATIVE = mod
+    return _NATIVE
 
 
-def _new(shape, dtype, like, stream):
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+def _on(stream, fn, *args):
+    """fn(*args) on `stream`: outputs are allocated there, tensors that belong to another stream are recorded."""
+    tensors = [a for a in args if isinstance(a, torch.Tensor)]
+    for t in tensors:
+        if t.is_cuda and t.get_device() != stream.device_index:
+            raise ValueError("the stream belongs to device %d, a tensor to %d" % (stream.device_index, t.get_device()))
+    with torch.cuda.device(stream.device_index):
+        other = torch.cuda.current_stream().cuda_stream != stream.cuda_stream
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _header_workspace(workspace, like, stream):
-    """The caller's workspace (its size is checked by the library), or a fresh zeroed header."""
-    if workspace is not None:
-        return workspace
-    if stream is None or not like.is_cuda:
-        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=like.device)
-
-
-def _enqueue(name, stream, *args):
-    """Call entry point `name` with `args` (tensors, integers or None, in the library's order; the first is a
-    tensor) and the stream, on the tensors' device."""
-    dev = args[0].get_device()
-    at = []
-    for a in args:
-        if type(a) is int or a is None:
-            at.append(a)
-        elif a.get_device() != dev or not a.is_contiguous() or dev < 0:
-            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
-        else:
-            at.append(a.data_ptr())
-    fn = getattr(_lib(), name)
-    raw = torch._C._cuda_getCurrentRawStream(dev)
-    if stream is not None:
-        if stream.device_index != dev:
-            raise ValueError("%s: the stream belongs to device %d, the tensors to %d" % (
-                name, stream.device_index, dev))
-        if stream.cuda_stream != raw:
-            raw = stream.cuda_stream
-            for a in args:
-                if isinstance(a, torch.Tensor):
-                    a.record_stream(stream)
-    if dev == torch._C._cuda_getDevice():
-        rc = fn(*at, raw)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*at, raw)
-    if rc:
-        _check(rc, name)
-
-
-def _out_type(out, out_dtype):
-    dt = out_dtype if out is None else out.dtype
-    if dt not in _OTYPE or (out is not None and out_dtype is not None and out_dtype != dt):
-        raise TypeError("the output must be bf16 or fp32 (and out of out_dtype), got %s" % dt)
-    return dt
-
-
-def _grouped(name, a, offsets, w, transpose, out, out_dtype, workspace, stream):
-    if w.dim() != 3 or a.dim() != 2:
-        raise ValueError("%s takes rows [rows, features] and weights [E, N, C]" % name)
-    E, N, C = w.shape
-    rows = a.shape[0]
-    ci, co = (N, C) if transpose else (C, N)
-    if a.dtype is not _BF16 or w.dtype is not _BF16 or offsets.dtype is not _I32 or a.shape[1] != ci or \
-            offsets.shape != (E + 1,):
-        _want("the row matrix", a, _BF16, (rows, ci))
-        _want("w", w, _BF16, (E, N, C))
-        _want("offsets", offsets, _I32, (E + 1,))
-    if out is None and out_dtype is None:
-        out_dtype = _BF16
-    dt = _out_type(out, out_dtype)
-    if out is None:
-        out = _new((rows, co), dt, a, stream)
-    elif out.shape != (rows, co):
-        _want("out", out, dt, (rows, co))
-    workspace = _header_workspace(workspace, a, stream)
-    _enqueue(name, stream, a, offsets, w, rows, N, C, E, _OTYPE[dt], out, workspace, workspace.nbytes)
+        out = fn(*args)
+    if other:
+        for t in tensors:
+            t.record_stream(stream)
     return out
+
+
+def _out_code(out_dtype):
+    code = _OTYPE.get(out_dtype)
+    if code is None:
+        raise TypeError("the output must be bf16 or fp32, got %s" % out_dtype)
+    return code
 
 
 def moe_grouped_mm(x, offsets, w, out=None, out_dtype=None, workspace=None, stream=None):
     """y [rows, N]: y[r] = w[e] x[r] for the rows [offsets[e], offsets[e+1]) of each expert e.
     x [rows, C] bf16, offsets [E+1] int32, w [E, N, C] bf16 -> bf16 (or out_dtype fp32).
     Rows of no expert are not written."""
-    return _grouped("moe_grouped_mm", x, offsets, w, False, out, out_dtype, workspace, stream)
+    fn = _native().grouped
+    if stream is not None:
+        return _on(stream, fn, False, x, offsets, w, out, _out_code(out_dtype), workspace)
+    return fn(False, x, offsets, w, out, _out_code(out_dtype), workspace)
 
 
 def moe_grouped_mm_dgrad(dy, offsets, w, out=None, out_dtype=None, workspace=None, stream=None):
     """dx [rows, C]: dx[r] = w[e]^T dy[r], the gradient of moe_grouped_mm's x.
     dy [rows, N] bf16, w [E, N, C] bf16 -> bf16 (or out_dtype fp32)."""
-    return _grouped("moe_grouped_mm_dgrad", dy, offsets, w, True, out, out_dtype, workspace, stream)
+    fn = _native().grouped
+    if stream is not None:
+        return _on(stream, fn, True, dy, offsets, w, out, _out_code(out_dtype), workspace)
+    return fn(True, dy, offsets, w, out, _out_code(out_dtype), workspace)
 
 
 def moe_grouped_mm_wgrad(dy, x, offsets, base=None, out=None, out_dtype=None, workspace=None, stream=None):
     """dw [E, N, C]: dw[e] = base[e] + sum over e's rows of dy[r] x[r]^T, the gradient of moe_grouped_mm's w.
     dy [rows, N] bf16, x [rows, C] bf16 -> bf16 (or fp32).  base [E, N, C] fp32 (fp32 output) may be
     `out` itself: the gradient is then accumulated in place.  Experts without rows get zeros (or base)."""
-    if dy.dim() != 2 or x.dim() != 2 or offsets.dim() != 1:
-        raise ValueError("moe_grouped_mm_wgrad takes rows [rows, N] and [rows, C] and offsets [E+1]")
-    rows, N = dy.shape
-    C, E = x.shape[1], offsets.shape[0] - 1
-    _want("dy", dy, _BF16, (rows, N))
-    _want("x", x, _BF16, (rows, C))
-    _want("offsets", offsets, _I32, (E + 1,))
-    if out is None and out_dtype is None:
-        out_dtype = _BF16 if base is None else _F32
-    dt = _out_type(out, out_dtype)
-    if base is not None:
-        if dt is not _F32:
-            raise TypeError("base needs an fp32 output")
-        _want("base", base, _F32, (E, N, C))
-    if out is None:
-        out = _new((E, N, C), dt, dy, stream)
-    else:
-        _want("out", out, dt, (E, N, C))
-        if base is not None and base.data_ptr() != out.data_ptr() and \
-                abs(base.data_ptr() - out.data_ptr()) < out.nbytes:
-            raise ValueError("base may be out itself, but must not overlap it otherwise")
-    workspace = _header_workspace(workspace, dy, stream)
-    _enqueue("moe_grouped_mm_wgrad", stream, dy, x, offsets, rows, N, C, E, _OTYPE[dt], base, out, workspace,
-             workspace.nbytes)
-    return out
-
-
-def _rows_args(row_weights, n_rows, rows):
-    if row_weights is not None:
-        _want("row_weights", row_weights, _F32, (rows,))
-    if n_rows is not None and (n_rows.dtype is not _I32 or n_rows.numel() != 1):
-        raise TypeError("n_rows must be one int32 on the device")
+    fn = _native().wgrad
+    if stream is not None:
+        return _on(stream, fn, dy, x, offsets, base, out, _out_code(out_dtype), workspace)
+    return fn(dy, x, offsets, base, out, _out_code(out_dtype), workspace)
 
 
 def moe_swiglu_checkpoint(gate_up, row_weights=None, n_rows=None, h=None, codes=None, scale=None, stream=None):
     """h = bf16(p * silu(g) * u) of gate_up [rows, 2F] bf16 (g | u) and row_weights p [rows] fp32, and its 8-bit
     checkpoint: codes [rows, 2F] uint8 (E4M3), scale [rows, 2F/128] fp32.  n_rows (one int32 on the device, e.g.
     offsets[-1:]): only the first n_rows rows are processed.  Returns (h, codes, scale)."""
-    if gate_up.dim() != 2 or gate_up.shape[1] % 256:
-        raise ValueError("gate_up must be [rows, 2F] with F a multiple of 128")
-    rows, F2 = gate_up.shape
-    F = F2 // 2
-    _want("gate_up", gate_up, _BF16, (rows, F2))
-    _rows_args(row_weights, n_rows, rows)
-    if h is None:
-        h = _new((rows, F), _BF16, gate_up, stream)
-    else:
-        _want("h", h, _BF16, (rows, F))
-    if codes is None:
-        codes = _new((rows, F2), torch.uint8, gate_up, stream)
-    else:
-        _codes("codes", codes, (rows, F2))
-    if scale is None:
-        scale = _new((rows, F // 64), _F32, gate_up, stream)
-    else:
-        _want("scale", scale, _F32, (rows, F // 64))
-    _enqueue("moe_swiglu_checkpoint", stream, gate_up, row_weights, n_rows, rows, F, h, codes, scale)
-    return h, codes, scale
+    fn = _native().checkpoint
+    if stream is not None:
+        return _on(stream, fn, gate_up, row_weights, n_rows, h, codes, scale)
+    return fn(gate_up, row_weights, n_rows, h, codes, scale)
 
 
 def moe_swiglu_checkpoint_backward(codes, scale, dh, row_weights=None, n_rows=None, dgate_up=None, h=None,
@@ -590,28 +500,11 @@ def moe_swiglu_checkpoint_backward(codes, scale, dh, row_weights=None, n_rows=No
     product's input taken before the row weight p.  Returns (dgate_up [rows, 2F] bf16, h [rows, F] bf16
     recomputed for the down weights' gradient, drow_weights [rows] fp32); want_h / want_drow_weights False
     leave those out (None)."""
-    if dh.dim() != 2 or dh.shape[1] % 128:
-        raise ValueError("dh must be [rows, F] with F a multiple of 128")
-    rows, F = dh.shape
-    _want("dh", dh, _BF16, (rows, F))
-    _codes("codes", codes, (rows, 2 * F))
-    _want("scale", scale, _F32, (rows, F // 64))
-    _rows_args(row_weights, n_rows, rows)
-    if dgate_up is None:
-        dgate_up = _new((rows, 2 * F), _BF16, dh, stream)
-    else:
-        _want("dgate_up", dgate_up, _BF16, (rows, 2 * F))
-    if h is not None:
-        _want("h", h, _BF16, (rows, F))
-    elif want_h:
-        h = _new((rows, F), _BF16, dh, stream)
-    if drow_weights is not None:
-        _want("drow_weights", drow_weights, _F32, (rows,))
-    elif want_drow_weights:
-        drow_weights = _new((rows,), _F32, dh, stream)
-    _enqueue("moe_swiglu_checkpoint_backward", stream, codes, scale, dh, row_weights, n_rows, rows, F, dgate_up, h,
-             drow_weights)
-    return dgate_up, h, drow_weights
+    fn = _native().checkpoint_backward
+    if stream is not None:
+        return _on(stream, fn, codes, scale, dh, row_weights, n_rows, dgate_up, h, drow_weights, want_h,
+                   want_drow_weights)
+    return fn(codes, scale, dh, row_weights, n_rows, dgate_up, h, drow_weights, want_h, want_drow_weights)
 
 
 def moe_permute_rows(x, inv, top_k_weights=None, x_scale=None, out=None, row_weights=None, stream=None):
@@ -619,61 +512,17 @@ def moe_permute_rows(x, inv, top_k_weights=None, x_scale=None, out=None, row_wei
     x [T, H] bf16, or E4M3 codes with x_scale [T, H/128]; inv [T, K] int32, negative = no row.
     out [n_rows, H] bf16 (default n_rows = T*K; rows no slot names are not written).
     Returns out, or (out, row_weights) with top_k_weights."""
-    if x.dim() != 2 or inv.dim() != 2:
-        raise ValueError("x must be [T, H] and inv [T, K]")
-    T, H = x.shape
-    K = inv.shape[1]
-    _want("inv", inv, _I32, (T, K))
-    if x_scale is None:
-        _want("x", x, _BF16, (T, H))
-    else:
-        _codes("x", x, (T, H))
-        _want("x_scale", x_scale, _F32, (T, H // 128))
-    if top_k_weights is not None:
-        _want("top_k_weights", top_k_weights, _F32, (T, K))
-    elif row_weights is not None:
-        raise ValueError("row_weights needs top_k_weights")
-    if out is None:
-        n_rows = T * K
-        out = _new((n_rows, H), _BF16, x, stream)
-    else:
-        n_rows = out.shape[0]
-        _want("out", out, _BF16, (n_rows, H))
-    if top_k_weights is not None:
-        if row_weights is None:
-            row_weights = _new((n_rows,), _F32, x, stream)
-        else:
-            _want("row_weights", row_weights, _F32, (n_rows,))
-    _enqueue("moe_permute_rows", stream, x, x_scale, inv, top_k_weights, K, T, H, n_rows, out, row_weights)
-    return out if row_weights is None else (out, row_weights)
+    fn = _native().permute
+    if stream is not None:
+        return _on(stream, fn, x, inv, top_k_weights, x_scale, out, row_weights)
+    return fn(x, inv, top_k_weights, x_scale, out, row_weights)
 
 
 def moe_unpermute_rows(y, inv, residual=None, drow_weights=None, out=None, dtop_k_weights=None, stream=None):
     """out [T, H] bf16 = sum over k ascending of y[inv[t,k]] (+ residual[t]), rounded once; with drow_weights
     [n_rows] fp32 also dtop_k_weights [T, K] = drow_weights[inv[t,k]].  y [n_rows, H] bf16 or fp32; slots whose
     inv is outside [0, n_rows) count as zero.  Returns out, or (out, dtop_k_weights)."""
-    if y.dim() != 2 or inv.dim() != 2:
-        raise ValueError("y must be [n_rows, H] and inv [T, K]")
-    n_rows, H = y.shape
-    T, K = inv.shape
-    if y.dtype not in _OTYPE:
-        raise TypeError("y must be bf16 or fp32, got %s" % y.dtype)
-    _want("inv", inv, _I32, (T, K))
-    if residual is not None:
-        _want("residual", residual, _BF16, (T, H))
-    if drow_weights is not None:
-        _want("drow_weights", drow_weights, _F32, (n_rows,))
-    elif dtop_k_weights is not None:
-        raise ValueError("dtop_k_weights needs drow_weights")
-    if out is None:
-        out = _new((T, H), _BF16, y, stream)
-    else:
-        _want("out", out, _BF16, (T, H))
-    if drow_weights is not None:
-        if dtop_k_weights is None:
-            dtop_k_weights = _new((T, K), _F32, y, stream)
-        else:
-            _want("dtop_k_weights", dtop_k_weights, _F32, (T, K))
-    _enqueue("moe_unpermute_rows", stream, y, _OTYPE[y.dtype], inv, residual, drow_weights, K, T, H, n_rows, out,
-             dtop_k_weights)
-    return out if drow_weights is None else (out, dtop_k_weights)
+    fn = _native().unpermute
+    if stream is not None:
+        return _on(stream, fn, y, inv, residual, drow_weights, out, dtop_k_weights)
+    return fn(y, inv, residual, drow_weights, out, dtop_k_weights)

@@ -1,14 +1,18 @@
-"""Build libmoe_b200.so in-tree with nvcc for sm_100a (B200)."""
+"""Build libmoe_b200.so in-tree with nvcc for sm_100a (B200), and the binding
+of the training operators (_native, a CPython extension on torch's headers)
+with g++."""
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_b200.so")
+BINDING = os.path.join(HERE, "_native.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -47,7 +51,28 @@ def build(force=False, verbose=False):
         subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp,
                                *objs, "-Xcompiler", "-fPIC"])
         os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
+
+
+def build_binding(force=False):
+    """_native.so from csrc/binding.cpp, linked to libmoe_b200.so beside it."""
+    src = os.path.join(CSRC, "binding.cpp")
+    header = os.path.join(HERE, "..", "include", "moe_b200.h")
+    if not (force or _stale(BINDING, [src, header])):
+        return BINDING
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.check_call(
+        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+         "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()), *["-isystem" + i for i in inc], src,
+         "-o", tmp, "-L" + HERE, "-l:libmoe_b200.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(root, "lib"),
+         "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ltorch_cuda"])
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

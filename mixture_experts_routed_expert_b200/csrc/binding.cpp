@@ -1,0 +1,355 @@
+// binding.cpp -- the Python side of the training step's operators: argument
+// checks, outputs and the call, as a CPython extension (_native).
+//
+// A training step makes dozens of these calls and the small ones run for two
+// or three microseconds on the GPU; checked and marshalled in Python through
+// ctypes a call took 8 us of host time, 5 of them before the library was
+// entered.  The library itself (libmoe_b200.so) stays a plain C ABI; this file
+// holds no arithmetic.
+//
+// Every function takes its arguments by position (the package's functions of
+// the same names, which document them, pass them on), works on the tensors'
+// device and that device's current stream, and raises TypeError / ValueError
+// for what the library could not see behind bare pointers.
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <ATen/ATen.h>
+#include <ATen/cuda/CUDAContext.h>
+#include <c10/cuda/CUDAGuard.h>
+
+#include <initializer_list>
+#include <sstream>
+#include <string>
+
+#include "../../include/moe_b200.h"
+
+namespace {
+
+using at::Tensor;
+
+struct Refusal {
+    PyObject *kind;
+    std::string what;
+};
+
+PyObject *g_check = nullptr;   // the package's _check(rc, what): raises MoEError
+
+const Tensor kNone;
+
+// A tensor argument, undefined for None.
+const Tensor &arg(PyObject *o, const char *what) {
+    if (o == Py_None) return kNone;
+    if (!THPVariable_Check(o)) throw Refusal{PyExc_TypeError, std::string(what) + " must be a tensor"};
+    return THPVariable_Unpack(o);
+}
+const Tensor &needed(PyObject *o, const char *what) {
+    const Tensor &t = arg(o, what);
+    if (!t.defined()) throw Refusal{PyExc_TypeError, std::string(what) + " must be a tensor"};
+    return t;
+}
+
+void dims(const Tensor &t, int64_t n, const char *what, const char *layout) {
+    if (t.dim() != n) throw Refusal{PyExc_ValueError, std::string(what) + " must be " + layout};
+}
+
+void shaped(const char *what, const Tensor &t, at::IntArrayRef shape) {
+    if (t.sizes() != shape) {
+        std::ostringstream s;
+        s << what << " must be " << shape << ", got " << t.sizes();
+        throw Refusal{PyExc_ValueError, s.str()};
+    }
+}
+
+// Where t is given: its type and shape.
+void want(const char *what, const Tensor &t, at::ScalarType type, at::IntArrayRef shape) {
+    if (!t.defined()) return;
+    if (t.scalar_type() != type) {
+        std::ostringstream s;
+        s << what << " must be " << type << ", got " << t.scalar_type();
+        throw Refusal{PyExc_TypeError, s.str()};
+    }
+    shaped(what, t, shape);
+}
+void want_codes(const char *what, const Tensor &t, at::IntArrayRef shape) {
+    if (!t.defined()) return;
+    if (t.scalar_type() != at::kByte && t.scalar_type() != at::kFloat8_e4m3fn)
+        throw Refusal{PyExc_TypeError, std::string(what) + " must be E4M3 codes (uint8 / float8_e4m3fn)"};
+    shaped(what, t, shape);
+}
+
+// All given tensors contiguous on one CUDA device: the device.
+int device_of(std::initializer_list<const Tensor *> all) {
+    int dev = -1;
+    for (const Tensor *t : all) {
+        if (!t->defined()) continue;
+        if (!t->is_cuda() || !t->is_contiguous() || (dev >= 0 && t->get_device() != dev))
+            throw Refusal{PyExc_ValueError, "all tensors must be contiguous CUDA tensors on one device"};
+        dev = (int)t->get_device();
+    }
+    return dev;
+}
+
+void *ptr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+const int32_t *i32(const Tensor &t) { return static_cast<const int32_t *>(ptr(t)); }
+float *f32(const Tensor &t) { return static_cast<float *>(ptr(t)); }
+void *stream_of(int dev) { return at::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
+
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor &like) {
+    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+}
+
+// The library takes sizes as int.
+int as_int(int64_t n) {
+    if (n > INT32_MAX) throw Refusal{PyExc_ValueError, "a dimension is over 2^31 - 1"};
+    return (int)n;
+}
+
+void check(int rc, const char *what) {
+    if (rc == MOE_OK) return;
+    PyObject *r = PyObject_CallFunction(g_check, "is", rc, what);
+    Py_XDECREF(r);
+    throw python_error();
+}
+
+// The caller's object where one was given, else a new one for the tensor.
+PyObject *given(PyObject *o, const Tensor &t) {
+    if (o != Py_None) {
+        Py_INCREF(o);
+        return o;
+    }
+    if (!t.defined()) Py_RETURN_NONE;
+    return THPVariable_Wrap(t);
+}
+
+at::ScalarType out_type(const Tensor &out, long asked, at::ScalarType otherwise) {
+    const at::ScalarType wish = asked == MOE_OUT_BF16 ? at::kBFloat16 : asked == MOE_OUT_FP32 ? at::kFloat : otherwise;
+    const at::ScalarType t = out.defined() ? out.scalar_type() : wish;
+    if ((t != at::kBFloat16 && t != at::kFloat) || (out.defined() && asked >= 0 && t != wish))
+        throw Refusal{PyExc_TypeError, "the output must be bf16 or fp32 (and out of out_dtype)"};
+    return t;
+}
+moe_otype_t otype(at::ScalarType t) { return t == at::kBFloat16 ? MOE_OUT_BF16 : MOE_OUT_FP32; }
+
+// The caller's workspace (its size is checked by the library), or a zeroed header.
+Tensor workspace_for(const Tensor &ws, const Tensor &like) {
+    return ws.defined() ? ws : at::zeros({8192}, at::TensorOptions().dtype(at::kByte).device(like.device()));
+}
+
+#define NATIVE_BEGIN(count)                                                      \
+    HANDLE_TH_ERRORS                                                             \
+    if (n != (count)) {                                                          \
+        PyErr_SetString(PyExc_TypeError, "wrong number of arguments");           \
+        return nullptr;                                                          \
+    }                                                                            \
+    try {
+#define NATIVE_END                                                               \
+    }                                                                            \
+    catch (const Refusal &r) {                                                   \
+        PyErr_SetString(r.kind, r.what.c_str());                                 \
+        return nullptr;                                                          \
+    }                                                                            \
+    END_HANDLE_TH_ERRORS
+
+// grouped(transpose, rows, offsets, w, out, out_type, workspace)
+PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    NATIVE_BEGIN(7)
+    const bool transpose = PyObject_IsTrue(a[0]);
+    const Tensor &x = needed(a[1], "the row matrix"), &off = needed(a[2], "offsets"), &w = needed(a[3], "w");
+    Tensor out = arg(a[4], "out");
+    dims(x, 2, "the row matrix", "[rows, features]");
+    dims(w, 3, "w", "[E, N, C]");
+    const int64_t rows = x.size(0), E = w.size(0), N = w.size(1), C = w.size(2);
+    const int64_t co = transpose ? C : N;
+    want("the row matrix", x, at::kBFloat16, {rows, transpose ? N : C});
+    want("w", w, at::kBFloat16, {E, N, C});
+    want("offsets", off, at::kInt, {E + 1});
+    const at::ScalarType t = out_type(out, PyLong_AsLong(a[5]), at::kBFloat16);
+    want("out", out, t, {rows, co});
+    const Tensor &given_ws = arg(a[6], "workspace");
+    const int dev = device_of({&x, &off, &w, &out, &given_ws});
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    if (!out.defined()) out = fresh({rows, co}, t, x);
+    const Tensor ws = workspace_for(given_ws, x);
+    check((transpose ? moe_grouped_mm_dgrad : moe_grouped_mm)(ptr(x), i32(off), ptr(w), as_int(rows), as_int(N),
+                                                              as_int(C), as_int(E), otype(t), ptr(out), ptr(ws),
+                                                              ws.nbytes(), stream_of(dev)),
+          transpose ? "moe_grouped_mm_dgrad" : "moe_grouped_mm");
+    return given(a[4], out);
+    NATIVE_END
+}
+
+// wgrad(dy, x, offsets, base, out, out_type, workspace)
+PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    NATIVE_BEGIN(7)
+    const Tensor &dy = needed(a[0], "dy"), &x = needed(a[1], "x"), &off = needed(a[2], "offsets");
+    const Tensor &base = arg(a[3], "base");
+    Tensor out = arg(a[4], "out");
+    dims(dy, 2, "dy", "[rows, N]");
+    dims(x, 2, "x", "[rows, C]");
+    dims(off, 1, "offsets", "[E+1]");
+    const int64_t rows = dy.size(0), N = dy.size(1), C = x.size(1), E = off.size(0) - 1;
+    want("dy", dy, at::kBFloat16, {rows, N});
+    want("x", x, at::kBFloat16, {rows, C});
+    want("offsets", off, at::kInt, {E + 1});
+    const at::ScalarType t = out_type(out, PyLong_AsLong(a[5]), base.defined() ? at::kFloat : at::kBFloat16);
+    if (base.defined() && t != at::kFloat) throw Refusal{PyExc_TypeError, "base needs an fp32 output"};
+    if (E < 0) throw Refusal{PyExc_ValueError, "offsets must be [E+1]"};
+    want("base", base, at::kFloat, {E, N, C});
+    want("out", out, t, {E, N, C});
+    const Tensor &given_ws = arg(a[6], "workspace");
+    const int dev = device_of({&dy, &x, &off, &base, &out, &given_ws});
+    if (base.defined() && out.defined()) {
+        const char *p = static_cast<const char *>(ptr(base)), *q = static_cast<const char *>(ptr(out));
+        const int64_t gap = p < q ? q - p : p - q;
+        if (gap != 0 && gap < (int64_t)out.nbytes())
+            throw Refusal{PyExc_ValueError, "base may be out itself, but must not overlap it otherwise"};
+    }
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    if (!out.defined()) out = fresh({E, N, C}, t, dy);
+    const Tensor ws = workspace_for(given_ws, dy);
+    check(moe_grouped_mm_wgrad(ptr(dy), ptr(x), i32(off), as_int(rows), as_int(N), as_int(C), as_int(E), otype(t),
+                               f32(base), ptr(out), ptr(ws), ws.nbytes(), stream_of(dev)),
+          "moe_grouped_mm_wgrad");
+    return given(a[4], out);
+    NATIVE_END
+}
+
+void want_rows(const Tensor &weights, const Tensor &n_rows, int64_t rows) {
+    want("row_weights", weights, at::kFloat, {rows});
+    if (n_rows.defined() && (n_rows.scalar_type() != at::kInt || n_rows.numel() != 1))
+        throw Refusal{PyExc_TypeError, "n_rows must be one int32 on the device"};
+}
+
+// checkpoint(gate_up, row_weights, n_rows, h, codes, scale)
+PyObject *checkpoint(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    NATIVE_BEGIN(6)
+    const Tensor &gu = needed(a[0], "gate_up"), &p = arg(a[1], "row_weights"), &live = arg(a[2], "n_rows");
+    Tensor h = arg(a[3], "h"), codes = arg(a[4], "codes"), scale = arg(a[5], "scale");
+    if (gu.dim() != 2 || gu.size(1) % 256)
+        throw Refusal{PyExc_ValueError, "gate_up must be [rows, 2F] with F a multiple of 128"};
+    const int64_t rows = gu.size(0), F = gu.size(1) / 2;
+    want("gate_up", gu, at::kBFloat16, {rows, 2 * F});
+    want_rows(p, live, rows);
+    want("h", h, at::kBFloat16, {rows, F});
+    want_codes("codes", codes, {rows, 2 * F});
+    want("scale", scale, at::kFloat, {rows, F / 64});
+    const int dev = device_of({&gu, &p, &live, &h, &codes, &scale});
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    if (!h.defined()) h = fresh({rows, F}, at::kBFloat16, gu);
+    if (!codes.defined()) codes = fresh({rows, 2 * F}, at::kByte, gu);
+    if (!scale.defined()) scale = fresh({rows, F / 64}, at::kFloat, gu);
+    check(moe_swiglu_checkpoint(ptr(gu), f32(p), i32(live), as_int(rows), as_int(F), ptr(h), ptr(codes), f32(scale),
+                                stream_of(dev)),
+          "moe_swiglu_checkpoint");
+    return Py_BuildValue("NNN", given(a[3], h), given(a[4], codes), given(a[5], scale));
+    NATIVE_END
+}
+
+// checkpoint_backward(codes, scale, dh, row_weights, n_rows, dgate_up, h, drow_weights, want_h, want_drow_weights)
+PyObject *checkpoint_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    NATIVE_BEGIN(10)
+    const Tensor &codes = needed(a[0], "codes"), &scale = needed(a[1], "scale"), &dh = needed(a[2], "dh");
+    const Tensor &p = arg(a[3], "row_weights"), &live = arg(a[4], "n_rows");
+    Tensor dgu = arg(a[5], "dgate_up"), h = arg(a[6], "h"), dp = arg(a[7], "drow_weights");
+    if (dh.dim() != 2 || dh.size(1) % 128)
+        throw Refusal{PyExc_ValueError, "dh must be [rows, F] with F a multiple of 128"};
+    const int64_t rows = dh.size(0), F = dh.size(1);
+    want("dh", dh, at::kBFloat16, {rows, F});
+    want_codes("codes", codes, {rows, 2 * F});
+    want("scale", scale, at::kFloat, {rows, F / 64});
+    want_rows(p, live, rows);
+    want("dgate_up", dgu, at::kBFloat16, {rows, 2 * F});
+    want("h", h, at::kBFloat16, {rows, F});
+    want("drow_weights", dp, at::kFloat, {rows});
+    const int dev = device_of({&codes, &scale, &dh, &p, &live, &dgu, &h, &dp});
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    if (!dgu.defined()) dgu = fresh({rows, 2 * F}, at::kBFloat16, dh);
+    if (!h.defined() && PyObject_IsTrue(a[8])) h = fresh({rows, F}, at::kBFloat16, dh);
+    if (!dp.defined() && PyObject_IsTrue(a[9])) dp = fresh({rows}, at::kFloat, dh);
+    check(moe_swiglu_checkpoint_backward(ptr(codes), f32(scale), ptr(dh), f32(p), i32(live), as_int(rows), as_int(F),
+                                         ptr(dgu), ptr(h), f32(dp), stream_of(dev)),
+          "moe_swiglu_checkpoint_backward");
+    return Py_BuildValue("NNN", given(a[5], dgu), given(a[6], h), given(a[7], dp));
+    NATIVE_END
+}
+
+// permute(x, inv, top_k_weights, x_scale, out, row_weights)
+PyObject *permute(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    NATIVE_BEGIN(6)
+    const Tensor &x = needed(a[0], "x"), &inv = needed(a[1], "inv"), &w = arg(a[2], "top_k_weights");
+    const Tensor &scale = arg(a[3], "x_scale");
+    Tensor out = arg(a[4], "out"), rw = arg(a[5], "row_weights");
+    dims(x, 2, "x", "[T, H]");
+    dims(inv, 2, "inv", "[T, K]");
+    const int64_t T = x.size(0), H = x.size(1), K = inv.size(1);
+    want("inv", inv, at::kInt, {T, K});
+    if (scale.defined()) {
+        want_codes("x", x, {T, H});
+        want("x_scale", scale, at::kFloat, {T, H / 128});
+    } else {
+        want("x", x, at::kBFloat16, {T, H});
+    }
+    want("top_k_weights", w, at::kFloat, {T, K});
+    if (rw.defined() && !w.defined()) throw Refusal{PyExc_ValueError, "row_weights needs top_k_weights"};
+    if (out.defined()) dims(out, 2, "out", "[n_rows, H]");
+    const int64_t rows = out.defined() ? out.size(0) : T * K;
+    want("out", out, at::kBFloat16, {rows, H});
+    want("row_weights", rw, at::kFloat, {rows});
+    const int dev = device_of({&x, &inv, &w, &scale, &out, &rw});
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    if (!out.defined()) out = fresh({rows, H}, at::kBFloat16, x);
+    if (w.defined() && !rw.defined()) rw = fresh({rows}, at::kFloat, x);
+    check(moe_permute_rows(ptr(x), f32(scale), i32(inv), f32(w), as_int(K), as_int(T), as_int(H), as_int(rows),
+                           ptr(out), f32(rw), stream_of(dev)),
+          "moe_permute_rows");
+    if (!w.defined()) return given(a[4], out);
+    return Py_BuildValue("NN", given(a[4], out), given(a[5], rw));
+    NATIVE_END
+}
+
+// unpermute(y, inv, residual, drow_weights, out, dtop_k_weights)
+PyObject *unpermute(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    NATIVE_BEGIN(6)
+    const Tensor &y = needed(a[0], "y"), &inv = needed(a[1], "inv"), &res = arg(a[2], "residual");
+    const Tensor &dr = arg(a[3], "drow_weights");
+    Tensor out = arg(a[4], "out"), dw = arg(a[5], "dtop_k_weights");
+    dims(y, 2, "y", "[n_rows, H]");
+    dims(inv, 2, "inv", "[T, K]");
+    const int64_t rows = y.size(0), H = y.size(1), T = inv.size(0), K = inv.size(1);
+    if (y.scalar_type() != at::kBFloat16 && y.scalar_type() != at::kFloat)
+        throw Refusal{PyExc_TypeError, "y must be bf16 or fp32"};
+    want("inv", inv, at::kInt, {T, K});
+    want("residual", res, at::kBFloat16, {T, H});
+    want("drow_weights", dr, at::kFloat, {rows});
+    if (dw.defined() && !dr.defined()) throw Refusal{PyExc_ValueError, "dtop_k_weights needs drow_weights"};
+    want("out", out, at::kBFloat16, {T, H});
+    want("dtop_k_weights", dw, at::kFloat, {T, K});
+    const int dev = device_of({&y, &inv, &res, &dr, &out, &dw});
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    if (!out.defined()) out = fresh({T, H}, at::kBFloat16, y);
+    if (dr.defined() && !dw.defined()) dw = fresh({T, K}, at::kFloat, y);
+    check(moe_unpermute_rows(ptr(y), otype(y.scalar_type()), i32(inv), ptr(res), f32(dr), as_int(K), as_int(T),
+                             as_int(H), as_int(rows), ptr(out), f32(dw), stream_of(dev)),
+          "moe_unpermute_rows");
+    if (!dr.defined()) return given(a[4], out);
+    return Py_BuildValue("NN", given(a[4], out), given(a[5], dw));
+    NATIVE_END
+}
+
+PyObject *set_check(PyObject *, PyObject *f) {
+    Py_INCREF(f);
+    Py_XSETREF(g_check, f);
+    Py_RETURN_NONE;
+}
+
+#define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
+PyMethodDef kMethods[] = {FAST(grouped),   FAST(wgrad),     FAST(checkpoint),
+                          FAST(checkpoint_backward), FAST(permute), FAST(unpermute),
+                          {"set_check", set_check, METH_O, nullptr},
+                          {nullptr, nullptr, 0, nullptr}};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__native(void) { return PyModule_Create(&kModule); }
