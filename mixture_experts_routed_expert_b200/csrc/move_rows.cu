@@ -51,8 +51,11 @@ __global__ void __launch_bounds__(kMaxThreads) permute_rows_kernel(
     }
 }
 
+// Six blocks of 256 on an SM (42 registers a thread): 2048 tokens x 6 slots x
+// 1280 columns 11.9 -> 9.9 us; batches of 8 slots (5 blocks) gain 3 % at
+// 8192 x 8 x 7168 and lose 16 % with 2 slots a token.
 template <bool F32>
-__global__ void __launch_bounds__(kMaxThreads) unpermute_rows_kernel(
+__global__ void __launch_bounds__(kMaxThreads, 6) unpermute_rows_kernel(
     const void *__restrict__ y, const int32_t *__restrict__ inv, const uint4 *__restrict__ residual,
     const float *__restrict__ drow, int T, int K, int V, int n_in, uint4 *__restrict__ out,
     float *__restrict__ dweights) {
