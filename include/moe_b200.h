@@ -439,10 +439,9 @@ MOE_API moe_status_t moe_debug_permute(const int32_t *top_k_index, int T, int K,
  * (gate_up: N = 2F, C = H; down: N = H, C = F).
  *
  *   x        [rows,C] bf16, dy [rows,N] bf16, w [E,N,C] bf16
- *   offsets  [E+1] int32 on the device, non-decreasing, within [0, rows]
- *            (values outside are clamped: the kernel reads and writes nothing
- *            outside the matrices, but decreasing offsets give some rows to
- *            two experts and leave the results of those rows undefined).
+ *   offsets  [E+1] int32 on the device, non-decreasing, within [0, rows].
+ *            Other values are made so: they are clamped, and a row that
+ *            several experts claim (decreasing offsets) is the first one's.
  *            Experts may be empty.  Rows before offsets[0] and from
  *            offsets[E] on belong to no expert: their outputs stay as they
  *            were and their values, whatever they hold, reach no sum.

@@ -26,6 +26,11 @@
 // stores by the CTA's threads would need a release to the other CTA, whose
 // fence (about 2000 cycles a tile) cost 13 us of 95 at 64 experts x 192 rows.
 //
+// With few tiles and a long reduction (split), clusters of 2 or 4 pairs share a
+// tile, each pair a stretch of its k-blocks; the partial sums meet in shared
+// memory and are added in the pairs' order, each pair finishing its share of
+// the rows: no scratch memory, no atomics, equal bits.
+//
 // Persistent: one CTA per SM, the pairs walk the tile list, which every CTA
 // derives from the offsets on the device.  Warp roles: 0 TMA producer of the
 // CTA's own operands (both CTAs' copies complete on the leading CTA's
@@ -86,6 +91,7 @@ struct MmArgs {
     int box_rows;             // rows per TMA box of a K-major B
     void *out;
     const float *base;        // weight gradient: added to the product (may be out itself), or null
+    int split;                // pairs of a cluster that share a tile
     int32_t *status;
 };
 
@@ -119,7 +125,7 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
 // ---- the pair: cluster barriers, remote arrivals, cta_group::2 tcgen05 -----
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -151,11 +157,18 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-// The address of the leading CTA's barrier at the same place as `bar`.
-__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
-    return a;
+// Shared-memory address `a` of this CTA as seen in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t addr_in(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+// The address of the pair's leading CTA's barrier at the same place as `bar`.
+__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) { return addr_in(smem_u32(bar), cluster_rank() & ~1u); }
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
 }
 // Arrive on the leading CTA's barrier.
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
@@ -202,7 +215,7 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << (cluster_rank() & ~1u)))
         : "memory");
 }
 
@@ -214,7 +227,7 @@ __device__ __forceinline__ void mma_commit_leader(uint64_t *bar) {
 
 template <int OP, int BN>
 __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t *s_beg, const int32_t *s_end,
-                                          const int32_t *s_tiles, int MT, int NT) {
+                                          const int32_t *s_tiles, int MT, int NT, int share) {
     MmTile t;
     if (OP == kWgrad) {
         t.e = w / (MT * NT);
@@ -247,6 +260,12 @@ __device__ __forceinline__ MmTile mm_tile(int w, const MmArgs &a, const int32_t 
         t.red0 = 0;
         t.red = a.red;
     }
+    if (a.split > 1) {       // this pair's k-blocks
+        const int KB = (t.red + kBK - 1) / kBK;
+        const int k0 = KB * share / a.split * kBK, k1 = KB * (share + 1) / a.split * kBK;
+        t.red0 += k0;
+        t.red = max(0, min(t.red, k1) - k0);
+    }
     return t;
 }
 
@@ -256,8 +275,10 @@ __device__ __forceinline__ bool ragged_end(const MmTile &t) {
     return OP == kWgrad && (t.red & 15);
 }
 
-template <int OP, bool OUT_BF16, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16, BN>::kThreads), 1)
+// SPLIT: clusters of args.split pairs, one tile a cluster (the grid has one for
+// every tile there can be); else pairs, which walk the tiles.
+template <int OP, bool OUT_BF16, int BN, bool SPLIT>
+__global__ void __launch_bounds__((MmCfg<OP, OUT_BF16, BN>::kThreads), 1)
     grouped_mm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ ZeroMaps zero, const MmArgs args) {
     using C = MmCfg<OP, OUT_BF16, BN>;
@@ -274,15 +295,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
     uint64_t *drained = rfull + C::kStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int32_t *s_part = reinterpret_cast<int32_t *>(tmem_slot + 2);          // [C::kThreads / 32]
+    int32_t *s_part = reinterpret_cast<int32_t *>(tmem_slot + 2);          // [64]: a maximum and a sum per warp
     uint8_t *s_out = smem + C::kRingBytes + 1024;
     int32_t *s_beg = reinterpret_cast<int32_t *>(smem + C::kRingBytes + 1024 + kOutStage);
     int32_t *s_end = s_beg + args.E;
     int32_t *s_tiles = s_end + args.E;                                      // [E+1]
 
     const int warp = threadIdx.x >> 5, lane = lane_id();
-    const int rank = (int)cluster_rank();      // 0: the leader
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr bool kSums = !OUT_BF16 || SPLIT; // the epilogue sums in registers
+    const int rank = (int)cluster_rank() & 1;  // 0: the pair's leader
+    const int share = SPLIT ? (int)cluster_rank() >> 1 : 0;
+    const int pair = blockIdx.x / (2 * args.split), pairs = gridDim.x / (2 * args.split);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -303,18 +326,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
     __syncwarp();
     cluster_arrive();                          // this CTA's barriers and TMEM are ready
     pdl_wait();
-    // Row ranges of the experts, clamped into the matrices whatever the
-    // offsets hold, and the prefix sum of their row tiles: each thread sums a
-    // run of experts, then warps and block are scanned.
+    // Row ranges of the experts and the prefix sum of their row tiles.  Whatever
+    // the offsets hold, the ranges lie within the matrices and do not overlap
+    // (each begins where the ones before it have ended, at the earliest), so
+    // that their tiles cannot be more than the rows allow.  Each thread takes a
+    // run of experts; sums (and, unless the offsets rise, maxima before them) are
+    // scanned over warps and block.
     const int per = (args.E + C::kThreads - 1) / C::kThreads;
     const int e0 = min(args.E, (int)threadIdx.x * per), e1 = min(args.E, e0 + per);
     int sum = 0;
+    bool rising = true;
     for (int e = e0; e < e1; ++e) {
-        const int b = min(max(__ldg(args.offsets + e), 0), args.rows);
-        const int n = min(max(__ldg(args.offsets + e + 1), b), args.rows);
-        s_beg[e] = b;
-        s_end[e] = n;
-        sum += (n - b + BN - 1) / BN;
+        s_beg[e] = min(max(__ldg(args.offsets + e), 0), args.rows);
+        s_end[e] = min(max(__ldg(args.offsets + e + 1), 0), args.rows);
+        rising = rising && s_beg[e] <= s_end[e];
+        sum += (s_end[e] - s_beg[e] + BN - 1) / BN;
+    }
+    if (!__syncthreads_and(rising)) {
+        int high = 0;
+        for (int e = e0; e < e1; ++e) high = max(high, s_end[e]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, high, o);
+            if (lane >= o) high = max(high, v);
+        }
+        if (lane == 31) s_part[32 + warp] = high;
+        high = __shfl_up_sync(0xFFFFFFFFu, high, 1);
+        if (lane == 0) high = 0;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) high = max(high, s_part[32 + i]);
+        sum = 0;
+        for (int e = e0; e < e1; ++e) {
+            s_beg[e] = max(s_beg[e], high);
+            high = max(high, s_end[e]);
+            s_end[e] = max(s_end[e], s_beg[e]);
+            sum += (s_end[e] - s_beg[e] + BN - 1) / BN;
+        }
     }
     int incl = sum;
 #pragma unroll
@@ -339,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
     const uint32_t tmem_base = *tmem_slot;
     const int MT = (args.M + kTM - 1) / kTM;
     const int NT = (args.N + BN - 1) / BN;
-    const int total = OP == kWgrad ? args.E * MT * NT : s_tiles[args.E] * MT;
+    const int total = OP == kWgrad ? args.E * MT * NT : s_tiles[args.E] * MT;   // with SPLIT at most `pairs`
     pdl_launch_dependents();
 
     if (warp == 0) {
@@ -351,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
             uint32_t used = 0, last = 0, rused = 0, rturn = 0;   // per stage: full in use yet, its last parity; rfull likewise
             bool ok = true;
             for (int w = pair; w < total && ok; w += pairs) {
-                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
+                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT, share);
                 if (t.nrows == 0) continue;
                 const int KB = (t.red + kBK - 1) / kBK;
                 const int half = ((t.nrows + 15) & ~15) / 2;         // B rows of each CTA
@@ -426,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
             const bool issuer = elect_one();
             bool ok = true;
             for (int w = pair; w < total && ok; w += pairs) {
-                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
+                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT, share);
                 if (t.nrows == 0 || t.red == 0) continue;
                 const int KB = (t.red + kBK - 1) / kBK;
                 const uint32_t idesc = idesc_bf16(kTM, (t.nrows + 15) & ~15) | kMajor;
@@ -438,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                 int stage = stage0;
                 uint32_t phase = phase0;
                 for (int i = 0; i < KB; ++i) {
-                    if (!OUT_BF16 && i > 0 && i % kPartBlocks == 0) {    // the next partial sum
+                    if (kSums && i > 0 && i % kPartBlocks == 0) {    // the next partial sum
                         if (issuer) mma_commit_pair(&tfull[acc]);
                         __syncwarp();
                         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
@@ -446,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                         tc_fence_after();
                         d = tmem_base + acc * BN;
                     }
-                    const bool first = OUT_BF16 ? i == 0 : i % kPartBlocks == 0;
+                    const bool first = kSums ? i % kPartBlocks == 0 : i == 0;
                     // the ragged k-block sits in the first stage; its turn comes after `delay` others
                     const bool ragged = ends_ragged && i == delay;
                     if (ends_ragged && i == 0 && !ragged && ++stage == C::kStages) { stage = 0; phase ^= 1; }
@@ -503,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
             int stage = 0;
             uint32_t turn = 0;
             for (int w = pair; w < total; w += pairs) {
-                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
+                const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT, share);
                 if (t.nrows == 0 || t.red == 0) continue;
                 const int KB = (t.red + kBK - 1) / kBK;
                 if (ragged_end<OP>(t)) {
@@ -537,10 +584,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int w = pair; w < total; w += pairs) {
-            const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT);
+            const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT, share);
             if (t.nrows == 0) continue;
             const bool none = OP == kWgrad && t.red == 0;     // an expert without rows: the sum is zero
-            if (none && args.base == args.out && args.base != nullptr) continue;
+            if (!SPLIT && none && args.base == args.out && args.base != nullptr) continue;
             const size_t orow = OP == kWgrad ? (size_t)t.e * args.N + t.row0 : (size_t)t.row0;
             const int mc = t.m0 + rank * kBM;   // first output column of this CTA
             const uint32_t lanes = tmem_base + ((uint32_t)(eg * 32) << 16);
@@ -550,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                 __syncwarp();
                 if (lane == 0) mbar_arrive_leader(&tempty[acc]);
             };
-            if (!OUT_BF16) {
+            if (kSums) {
                 // This lane's output column, NI times 32 rows of it in registers: the
                 // base to begin with (asked for before the product is there, and
                 // wholly read before any store: it may be out itself), plus each
@@ -559,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                 float sum[NI][32];
                 const bool mine = mc + eg * 32 + lane < args.M;
                 const size_t at0 = orow * args.M + mc + eg * 32 + lane;
-                const bool based = OP == kWgrad && args.base != nullptr && mine;
+                const bool based = OP == kWgrad && !SPLIT && args.base != nullptr && mine;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const int c0 = (set + C::kSets * i) * 32;
@@ -598,6 +645,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
                     *abort_flag = 1;
                     atomicOr(args.status, DEV_TIMEOUT);
                     break;
+                }
+                if (SPLIT) {     // to shared memory, the ring's: [row][128 columns]
+                    float *part = reinterpret_cast<float *>(ring) + eg * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int c0 = (set + C::kSets * i) * 32;
+                        if (c0 >= t.nrows) break;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) part[(c0 + j) * kBM] = sum[i][j];
+                    }
+                    continue;
                 }
                 // one check per 32 rows: a compare, a branch and a 64-bit product a
                 // store made 600 instructions of them and held the stores at 3 TB/s
@@ -676,6 +734,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((MmCfg<OP, OUT_BF16,
     tc_fence_before();
     __syncthreads();
     __syncwarp();
+    if (SPLIT) {
+        cluster_arrive();
+        cluster_wait();                        // every pair's partial sums are in place
+        if (pair < total && warp >= 2 && warp < 2 + C::kEpiWarps) {
+            const MmTile t = mm_tile<OP, BN>(pair, args, s_beg, s_end, s_tiles, MT, NT, share);
+            const size_t orow = OP == kWgrad ? (size_t)t.e * args.N + t.row0 : (size_t)t.row0;
+            const int m = t.m0 + rank * kBM + lane * 4, step = args.split * C::kEpiWarps;
+            constexpr int kRows = BN == 256 ? 4 : 2;          // rows of a warp in flight
+            for (int j0 = share + args.split * (warp - 2); j0 < t.nrows; j0 += kRows * step) {
+                float4 v[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const int j = j0 + r * step;
+                    v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (OP == kWgrad && args.base && j < t.nrows && m < args.M)
+                        v[r] = *reinterpret_cast<const float4 *>(args.base + (orow + j) * args.M + m);
+                }
+                for (int q = 0; q < args.split; ++q) {
+                    const uint32_t from = addr_in(smem_u32(ring), 2 * q + rank) + lane * 16;
+                    float4 p[kRows];
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) p[r] = ld_cluster4(from + min(j0 + r * step, t.nrows - 1) * (kBM * 4));
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        v[r].x += p[r].x; v[r].y += p[r].y; v[r].z += p[r].z; v[r].w += p[r].w;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const int j = j0 + r * step;
+                    const size_t at = (orow + j) * args.M + m;
+                    if (j >= t.nrows || m >= args.M) continue;
+                    if (OUT_BF16)
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(args.out) + at) =
+                            make_uint2(pack_bf16x2(v[r].x, v[r].y), pack_bf16x2(v[r].z, v[r].w));
+                    else
+                        *reinterpret_cast<float4 *>(static_cast<float *>(args.out) + at) = v[r];
+                }
+            }
+        }
+        __syncwarp();
+    }
     cluster_arrive();
     cluster_wait();
     if (warp == 1) {
@@ -713,20 +813,83 @@ bool make_tmap_zero(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t col
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int OP, bool OUT_BF16, int BN>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const ZeroMaps &z, const MmArgs &args, cudaStream_t st) {
+// A kernel's launch in clusters of `split` pairs.
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    ClusterLaunch(int ctas, int threads, size_t smem, int split, cudaStream_t st) {
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2 * split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+template <int OP, bool OUT_BF16, int BN, bool SPLIT>
+cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const ZeroMaps &z, const MmArgs &args, int ctas,
+                   cudaStream_t st) {
     using C = MmCfg<OP, OUT_BF16, BN>;
+    auto *kernel = grouped_mm<OP, OUT_BF16, BN, SPLIT>;
     static std::atomic<int> attr_done[64];
-    const cudaError_t e = enable_max_dyn_smem((const void *)grouped_mm<OP, OUT_BF16, BN>, attr_done);
+    const cudaError_t e = enable_max_dyn_smem((const void *)kernel, attr_done);
     if (e != cudaSuccess) return e;
-    return launch_k(grouped_mm<OP, OUT_BF16, BN>, dim3(num_sms() & ~1), dim3(C::kThreads), C::smem_bytes(args.E), st,
-                    true, a, b, z, args);
+    ClusterLaunch l(ctas, C::kThreads, C::smem_bytes(args.E), args.split, st);
+    return cudaLaunchKernelEx(&l.cfg, kernel, a, b, z, args);
+}
+
+// Clusters of `split` pairs that the current device runs at once, one CTA per
+// SM (asked once per device: the GPU's processor clusters are not all alike).
+int clusters_at_once(int split) {
+    using C = MmCfg<kFwd, true, 256>;
+    auto *kernel = grouped_mm<kFwd, true, 256, true>;
+    static std::atomic<int> attr_done[64];
+    static std::atomic<int> cache[64][2];   // 0: not asked yet; -1: none
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::atomic<int> &c = cache[dev & 63][split == 4];
+    int n = c.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (enable_max_dyn_smem((const void *)kernel, attr_done) != cudaSuccess) return 0;
+        ClusterLaunch l(2 * split, C::kThreads, C::smem_bytes(1), split, nullptr);
+        l.cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            n = -1;
+        }
+        c.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Pairs that share a tile, for at most `tiles` tiles of about `blocks` k-blocks:
+// 4 or 2 where the clusters run at once and the k-blocks saved, 0.26 us each,
+// are worth more than the joining.
+int split_of(int64_t tiles, int64_t blocks, int bn) {
+    const int worth = bn == 64 ? 16 : 32;
+    if (tiles > 37 || blocks < worth) return 1;
+    if (tiles <= clusters_at_once(4)) return 4;
+    return blocks >= 2 * worth && tiles <= clusters_at_once(2) ? 2 : 1;
 }
 
 template <int OP, int BN>
-cudaError_t launch(bool out_bf16, const CUtensorMap &a, const CUtensorMap &b, const ZeroMaps &z, const MmArgs &args,
-                   cudaStream_t st) {
-    return out_bf16 ? launch<OP, true, BN>(a, b, z, args, st) : launch<OP, false, BN>(a, b, z, args, st);
+cudaError_t launch(bool out_bf16, const CUtensorMap &a, const CUtensorMap &b, const ZeroMaps &z, MmArgs args,
+                   int64_t tiles, int64_t blocks, cudaStream_t st) {
+    args.split = split_of(tiles, blocks, BN);
+    if (args.split > 1) {
+        const int ctas = (int)tiles * 2 * args.split;
+        return out_bf16 ? launch<OP, true, BN, true>(a, b, z, args, ctas, st)
+                        : launch<OP, false, BN, true>(a, b, z, args, ctas, st);
+    }
+    const int ctas = num_sms() & ~1;
+    return out_bf16 ? launch<OP, true, BN, false>(a, b, z, args, ctas, st)
+                    : launch<OP, false, BN, false>(a, b, z, args, ctas, st);
 }
 
 }  // namespace
@@ -749,9 +912,14 @@ cudaError_t launch_grouped_mm(const void *x, const void *w, const int32_t *offse
         !make_tmap(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, rows, red, a.box_rows))
         return cudaErrorInvalidValue;
     const ZeroMaps z = {};   // not used by these two
+    // at most one partly filled row tile for each expert that can have rows
+    const int64_t tiles = ((int64_t)std::min(rows, E) + rows / (few ? 64 : 256)) * ((a.M + kTM - 1) / kTM);
+    const int64_t blocks = (red + kBK - 1) / kBK;
     if (transpose)
-        return few ? launch<kDgrad, 64>(out_bf16, ta, tb, z, a, st) : launch<kDgrad, 256>(out_bf16, ta, tb, z, a, st);
-    return few ? launch<kFwd, 64>(out_bf16, ta, tb, z, a, st) : launch<kFwd, 256>(out_bf16, ta, tb, z, a, st);
+        return few ? launch<kDgrad, 64>(out_bf16, ta, tb, z, a, tiles, blocks, st)
+                   : launch<kDgrad, 256>(out_bf16, ta, tb, z, a, tiles, blocks, st);
+    return few ? launch<kFwd, 64>(out_bf16, ta, tb, z, a, tiles, blocks, st)
+               : launch<kFwd, 256>(out_bf16, ta, tb, z, a, tiles, blocks, st);
 }
 
 cudaError_t launch_grouped_wgrad(const void *dy, const void *x, const int32_t *offsets, int rows, int N, int C, int E,
@@ -771,7 +939,8 @@ cudaError_t launch_grouped_wgrad(const void *dy, const void *x, const int32_t *o
         !make_tmap(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, rows, N, kBK) ||
         !make_tmap_zero(&z.rows4, x, rows, C, 4) || !make_tmap_zero(&z.rows1, x, rows, C, 1))
         return cudaErrorInvalidValue;
-    return launch<kWgrad, 256>(out_bf16, ta, tb, z, a, st);
+    const int64_t tiles = (int64_t)E * ((N + 255) / 256) * ((C + kTM - 1) / kTM);
+    return launch<kWgrad, 256>(out_bf16, ta, tb, z, a, tiles, rows / E / kBK, st);
 }
 
 }  // namespace moe

@@ -14,12 +14,13 @@ def offsets_of(counts, first=0):
 
 
 def spans(offsets, rows):
-    """(expert, first row, end) with the documented clamping."""
-    out = []
-    o = offsets.tolist()
+    """(expert, first row, end) as documented: clamped, a row that several claim the first one's."""
+    out, high = [], 0
+    o = [min(max(v, 0), rows) for v in offsets.tolist()]
     for e in range(len(o) - 1):
-        b = min(max(o[e], 0), rows)
-        out.append((e, b, min(max(o[e + 1], b), rows)))
+        b = max(o[e], high)
+        high = max(high, o[e + 1])
+        out.append((e, b, max(o[e + 1], b)))
     return out
 
 

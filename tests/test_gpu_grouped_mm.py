@@ -113,6 +113,75 @@ def test_offsets_outside_the_rows_are_clamped(moe, cuda_dev):
     check_sum(moe.moe_grouped_mm_wgrad(dd, xd, o), *wgrad64(dy, x, off), 10)
 
 
+@pytest.mark.parametrize("off", [[0, 12, 5, 20], [20, 0, 20, 0, 20], [7, 7, 3, 100, -2 ** 31, 2 ** 31 - 1]])
+def test_rows_claimed_twice_are_the_first_ones(moe, cuda_dev, off):
+    off = torch.tensor(off, dtype=torch.int32)
+    E = len(off) - 1
+    _, x, dy, _ = _inputs([20], 40, 72, seed=3)
+    w = (torch.randn(E, 40, 72, generator=torch.Generator().manual_seed(4)) * 0.1).to(BF)
+    o, xd, dd, wd = (t.to(cuda_dev) for t in (off, x, dy, w))
+    y = torch.zeros(20, 40, dtype=F32, device=cuda_dev)
+    dx = torch.zeros(20, 72, dtype=F32, device=cuda_dev)
+    check_sum(moe.moe_grouped_mm(xd, o, wd, out=y), *mm64(x, off, w, False), 72)
+    check_sum(moe.moe_grouped_mm_dgrad(dd, o, wd, out=dx), *mm64(dy, off, w, True), 40)
+    check_sum(moe.moe_grouped_mm_wgrad(dd, xd, o), *wgrad64(dy, x, off), 20)
+
+
+# Few tiles and long reductions: 4 or 2 pairs of a cluster share a tile (for
+# 64-row tiles from 16 / 32 k-blocks of 64 on, for 256-row tiles from 32 / 64).
+SPLITS = [
+    ([5], 64, 1024), ([5], 64, 1032), ([64, 0, 3], 136, 2056), ([1], 8, 7168),      # 64 rows, 4 pairs
+    ([1, 2, 0, 3, 1], 1032, 2056),                                                   # 64 rows, 2 pairs
+    ([300], 72, 2056), ([200, 129], 264, 2120),                                      # 256 rows, 4 pairs
+    ([200, 150, 301, 149], 1000, 4104),                                              # 256 rows, 2 pairs
+    ([300], 72, 1288), ([9, 1], 1544, 520),                                          # not shared
+]
+
+
+@pytest.mark.parametrize("counts,N,C", SPLITS)
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_tiles_shared_by_pairs(moe, cuda_dev, counts, N, C, dt):
+    off, x, dy, w = _inputs(counts, N, C, slack=3, seed=14)
+    n = sum(counts)
+    o, xd, wd = off.to(cuda_dev), x.to(cuda_dev), w.to(cuda_dev)
+    ws = torch.zeros(8192, dtype=torch.uint8, device=cuda_dev)
+    y = torch.full((n + 3, N), -3.0, dtype=dt, device=cuda_dev)
+    moe.moe_grouped_mm(xd, o, wd, out=y, workspace=ws)
+    ref, mag = mm64(x, off, w, False)
+    check_sum(y[:n], ref[:n], mag[:n], C, "forward")
+    # the same shapes the other way round: dy [rows, C], w [E, C, N]
+    wt = wd.transpose(1, 2).contiguous()
+    dx = torch.full((n + 3, N), -3.0, dtype=dt, device=cuda_dev)
+    moe.moe_grouped_mm_dgrad(xd, o, wt, out=dx, workspace=ws)
+    check_sum(dx[:n], ref[:n], mag[:n], C, "input gradient")
+    assert (y[n:] == -3).all() and (dx[n:] == -3).all()
+    assert torch.equal(moe.moe_grouped_mm(xd, o, wd, out_dtype=dt, workspace=ws)[:n], y[:n])
+    assert moe.moe_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("counts,N,C", [([2100], 72, 136), ([4200, 100], 264, 520), ([1, 9000, 700, 0], 8, 16),
+                                        ([0, 4300], 512, 512),                       # 4 pairs
+                                        ([4111], 1032, 1032),                        # 2 pairs
+                                        ([1100], 72, 136), ([515, 514], 512, 512)])  # not shared
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_weight_gradients_shared_by_pairs(moe, cuda_dev, counts, N, C, dt):
+    off, x, dy, _ = _inputs(counts, N, C, first=2, slack=5, seed=15)
+    x[:2], x[-5:], dy[:2], dy[-5:] = float("nan"), float("inf"), float("inf"), float("nan")
+    o, xd, dd = off.to(cuda_dev), x.to(cuda_dev), dy.to(cuda_dev)
+    ws = torch.zeros(8192, dtype=torch.uint8, device=cuda_dev)
+    x[:2], x[-5:], dy[:2], dy[-5:] = 0, 0, 0, 0
+    check_sum(moe.moe_grouped_mm_wgrad(dd, xd, o, out_dtype=dt, workspace=ws), *wgrad64(dy, x, off), max(counts))
+    if dt == F32:
+        base = torch.randn(len(counts), N, C, generator=torch.Generator().manual_seed(16))
+        bd = base.to(cuda_dev)
+        ref, mag = wgrad64(dy, x, off, base)
+        new = moe.moe_grouped_mm_wgrad(dd, xd, o, base=bd, workspace=ws)
+        check_sum(new, ref, mag, max(counts) + 1, "with base")
+        moe.moe_grouped_mm_wgrad(dd, xd, o, base=bd, out=bd, workspace=ws)
+        assert torch.equal(bd, new)
+    assert moe.moe_workspace_status(ws) == 0
+
+
 def test_many_experts(moe, cuda_dev):
     counts = [(7 * e) % 3 for e in range(1024)]
     off, x, dy, w = _inputs(counts, 16, 24, seed=5)
