@@ -9,9 +9,10 @@
 //
 // One kernel serves the three, two CTAs of a cluster on one 256 x 256 tile
 // (cta_group::2): each holds 128 columns of the A operand and half of the B
-// operand, and 128 x 256 of the accumulator.  The A operand (MMA M) is the
-// side that is contiguous in the output, the B operand (MMA N) the other, so that the 32 lanes of an epilogue warp always hold 32
-// neighbouring output columns:
+// operand, and 128 x 256 of the accumulator.  (One CTA on 128 x 256 read half
+// as much again from L2.)  The A operand (MMA M) is the side that is contiguous
+// in the output, the B operand (MMA N) the other, so that the 32 lanes of an
+// epilogue warp always hold 32 neighbouring output columns:
 //   forward          A = w[e]  (reduction contiguous: "K-major")   B = x rows  (K-major)
 //   input gradient   A = w[e]  (output side contiguous: "MN-major") B = dy rows (K-major)
 //   weight gradient  A = x     (MN-major)                           B = dy      (MN-major)
@@ -25,6 +26,15 @@
 // TMA writes those zeros too, as boxes that lie wholly outside the matrix:
 // stores by the CTA's threads would need a release to the other CTA, whose
 // fence (about 2000 cycles a tile) cost 13 us of 95 at 64 experts x 192 rows.
+//
+// What bounds it.  Large products: power; 16384 rows on 32 experts, N=4096
+// C=7168, run the tensor pipe 91 % of the time that tiles are there, at 1.5 GHz
+// (forward 760 us from a cool start, 890 under load: 1.08 PFLOP/s; one expert of
+// as many rows 715 us, what a plain library product of that size takes).  The
+// MMAs of a stage and its TMA loads have to come from elected threads: issued
+// by a thread picked by its lane number they paced the kernel at 1140 us.
+// Few rows: the weights' way through L2 (64 experts, 2048 rows: 294 MB in 55 us).
+// Weight gradients of short reductions: writing dw, at 4.5 TB/s.
 //
 // With few tiles and a long reduction (split), clusters of 2 or 4 pairs share a
 // tile, each pair a stretch of its k-blocks; the partial sums meet in shared
@@ -903,7 +913,11 @@ cudaError_t launch_grouped_mm(const void *x, const void *w, const int32_t *offse
     a.E = E;
     a.M = transpose ? C : N;
     a.red = red;
-    const bool few = rows <= (int64_t)32 * E;
+    // 64-row tiles (nine stages of weights in flight, not six) up to 16 rows an
+    // expert: 64 experts, N=1792 C=1280, 64 / 256 rows: 6 rows 10.5 / 12.9 us,
+    // 1024 rows 52.2 / 53.1 us; at 2048 rows even experts 55.1 / 56.6 us, but
+    // Zipf(1.1) experts 51.2 / 49.2 us, and 66.8 / 56.7 us at 4096.
+    const bool few = rows <= (int64_t)16 * E;
     a.box_rows = few ? 32 : 128;   // at most BN / 2: the boxes of a stage lie within its B region
     a.out = out;
     a.status = status;

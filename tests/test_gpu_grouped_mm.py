@@ -130,9 +130,9 @@ def test_rows_claimed_twice_are_the_first_ones(moe, cuda_dev, off):
 # Few tiles and long reductions: 4 or 2 pairs of a cluster share a tile (for
 # 64-row tiles from 16 / 32 k-blocks of 64 on, for 256-row tiles from 32 / 64).
 SPLITS = [
-    ([5], 64, 1024), ([5], 64, 1032), ([64, 0, 3], 136, 2056), ([1], 8, 7168),      # 64 rows, 4 pairs
+    ([5], 64, 1024), ([5], 64, 1032), ([40, 0, 3, 2], 136, 2056), ([1], 8, 7168),   # 64 rows, 4 pairs
     ([1, 2, 0, 3, 1], 1032, 2056),                                                   # 64 rows, 2 pairs
-    ([300], 72, 2056), ([200, 129], 264, 2120),                                      # 256 rows, 4 pairs
+    ([64, 0, 3], 136, 2056), ([300], 72, 2056), ([200, 129], 264, 2120),                                      # 256 rows, 4 pairs
     ([200, 150, 301, 149], 1000, 4104),                                              # 256 rows, 2 pairs
     ([300], 72, 1288), ([9, 1], 1544, 520),                                          # not shared
 ]
