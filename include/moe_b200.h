@@ -410,7 +410,7 @@ MOE_API moe_status_t quantize_fp8_block128(const void *x, int rows, int cols, vo
 /*
  * Expert histogram and stable permutation of the T*K routing slots
  * (slot = t*K + k), exposed for exact testing of the step the prefill path
- * runs first.
+ * runs first, and as the plan of the training operators (offsets, inv).
  *   counts  [E]    slots routed to each expert
  *   offsets [E+1]  exclusive prefix sum of counts
  *   perm    [T*K]  slot at each permuted position; positions of one expert

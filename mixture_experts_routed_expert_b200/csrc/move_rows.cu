@@ -6,6 +6,11 @@
 // Each is the other's transpose, so each is also the other's gradient.  Both
 // go token by token: permute reads a token's row once and writes it K times,
 // unpermute reads its K rows and writes one.
+//
+// What bounds them: memory.  8192 tokens x 8 slots x 7168 columns: permute from
+// codes 171 us for 1.0 GB, unpermute 182 us for 1.2 GB (5.8 and 6.5 TB/s); 2047
+// tokens 46 us.  2048 tokens x 6 x 1280 (42 MB): unpermute 9.9 us, of which 6.4
+// are the bytes.
 #include "common.cuh"
 #include "internal.h"
 

@@ -11,6 +11,13 @@
 // Since h carries p, dh (the gradient of the down product's input before p)
 // gives p's gradient by one dot product per row and the expert output need
 // not be kept.
+//
+// What bounds them: memory, one pass over each array.  65536 rows x F=2048:
+// forward 178 us for 1.08 GB (6.1 TB/s, 0.92 of a copy's rate), backward 220 us
+// for 1.35 GB (0.94).  Instructions come second: with one fp32 operation at a
+// time, library exponentials and quotients and a division per vector for the
+// index the forward issued 346 instructions for 8 pairs of values and took
+// 250 us.  A few rows (96 x 896): 2.4 us, the latency of one load and a launch.
 #include <float.h>
 
 #include "common.cuh"
