@@ -512,7 +512,7 @@ MOE_API moe_status_t moe_swiglu_checkpoint_backward(const void *codes, const flo
  *       top_k_weights[t,k].  x [T,H] bf16, or with x_scale [T,H/128] fp32
  *       (H % 128 == 0) E4M3 codes of quantize_fp8_block128, restored as
  *       bf16(code * scale).  Positions must be distinct (two slots with one
- *       position leave either slot's values there); rows that no slot names
+ *       position leave a mix of their values there); rows that no slot names
  *       stay as they were.  top_k_weights and row_weights: both or neither.
  *   moe_unpermute_rows  out[t] = bf16(sum over k ascending of y[inv[t,k]] +
  *       residual[t]), summed in fp32; dtop_k_weights[t,k] =

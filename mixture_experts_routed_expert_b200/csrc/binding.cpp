@@ -90,6 +90,26 @@ int device_of(std::initializer_list<const Tensor *> all) {
     return dev;
 }
 
+// No output may overlap an input or another output.
+void apart(std::initializer_list<const Tensor *> outs, std::initializer_list<const Tensor *> ins) {
+    struct Range {
+        uintptr_t from, to;
+    } r[16];
+    size_t n = 0, n_outs = 0;
+    auto add = [&](const Tensor *t) {
+        if (!t->defined()) return;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t->const_data_ptr());
+        r[n++] = {p, p + t->nbytes()};
+    };
+    for (const Tensor *t : outs) add(t);
+    n_outs = n;
+    for (const Tensor *t : ins) add(t);
+    for (size_t o = 0; o < n_outs; ++o)
+        for (size_t i = o + 1; i < n; ++i)
+            if (r[o].from < r[i].to && r[i].from < r[o].to)
+                throw Refusal{PyExc_ValueError, i < n_outs ? "two outputs overlap" : "an output overlaps an input"};
+}
+
 void *ptr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 const int32_t *i32(const Tensor &t) { return static_cast<const int32_t *>(ptr(t)); }
 float *f32(const Tensor &t) { return static_cast<float *>(ptr(t)); }
@@ -168,6 +188,7 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
     want("out", out, t, {rows, co});
     const Tensor &given_ws = arg(a[6], "workspace");
     const int dev = device_of({&x, &off, &w, &out, &given_ws});
+    apart({&out}, {&x, &off, &w, &given_ws});
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
     if (!out.defined()) out = fresh({rows, co}, t, x);
     const Tensor ws = workspace_for(given_ws, x);
@@ -199,12 +220,8 @@ PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     want("out", out, t, {E, N, C});
     const Tensor &given_ws = arg(a[6], "workspace");
     const int dev = device_of({&dy, &x, &off, &base, &out, &given_ws});
-    if (base.defined() && out.defined()) {
-        const char *p = static_cast<const char *>(ptr(base)), *q = static_cast<const char *>(ptr(out));
-        const int64_t gap = p < q ? q - p : p - q;
-        if (gap != 0 && gap < (int64_t)out.nbytes())
-            throw Refusal{PyExc_ValueError, "base may be out itself, but must not overlap it otherwise"};
-    }
+    // base may be out itself
+    apart({&out}, {&dy, &x, &off, &given_ws, base.defined() && out.defined() && ptr(base) == ptr(out) ? &kNone : &base});
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
     if (!out.defined()) out = fresh({E, N, C}, t, dy);
     const Tensor ws = workspace_for(given_ws, dy);
@@ -235,6 +252,7 @@ PyObject *checkpoint(PyObject *, PyObject *const *a, Py_ssize_t n) {
     want_codes("codes", codes, {rows, 2 * F});
     want("scale", scale, at::kFloat, {rows, F / 64});
     const int dev = device_of({&gu, &p, &live, &h, &codes, &scale});
+    apart({&h, &codes, &scale}, {&gu, &p, &live});
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
     if (!h.defined()) h = fresh({rows, F}, at::kBFloat16, gu);
     if (!codes.defined()) codes = fresh({rows, 2 * F}, at::kByte, gu);
@@ -263,6 +281,7 @@ PyObject *checkpoint_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     want("h", h, at::kBFloat16, {rows, F});
     want("drow_weights", dp, at::kFloat, {rows});
     const int dev = device_of({&codes, &scale, &dh, &p, &live, &dgu, &h, &dp});
+    apart({&dgu, &h, &dp}, {&codes, &scale, &dh, &p, &live});
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
     if (!dgu.defined()) dgu = fresh({rows, 2 * F}, at::kBFloat16, dh);
     if (!h.defined() && PyObject_IsTrue(a[8])) h = fresh({rows, F}, at::kBFloat16, dh);
@@ -297,6 +316,7 @@ PyObject *permute(PyObject *, PyObject *const *a, Py_ssize_t n) {
     want("out", out, at::kBFloat16, {rows, H});
     want("row_weights", rw, at::kFloat, {rows});
     const int dev = device_of({&x, &inv, &w, &scale, &out, &rw});
+    apart({&out, &rw}, {&x, &inv, &w, &scale});
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
     if (!out.defined()) out = fresh({rows, H}, at::kBFloat16, x);
     if (w.defined() && !rw.defined()) rw = fresh({rows}, at::kFloat, x);
@@ -326,6 +346,7 @@ PyObject *unpermute(PyObject *, PyObject *const *a, Py_ssize_t n) {
     want("out", out, at::kBFloat16, {T, H});
     want("dtop_k_weights", dw, at::kFloat, {T, K});
     const int dev = device_of({&y, &inv, &res, &dr, &out, &dw});
+    apart({&out, &dw}, {&y, &inv, &res, &dr});
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
     if (!out.defined()) out = fresh({T, H}, at::kBFloat16, y);
     if (dr.defined() && !dw.defined()) dw = fresh({T, K}, at::kFloat, y);

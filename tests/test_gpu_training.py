@@ -202,3 +202,27 @@ def test_refusals(training, cuda_dev):
                 lambda: training.experts_backward(saved, out, gu, dn, ddown=torch.zeros_like(dn))):
         with pytest.raises(TypeError):
             bad()
+
+
+def test_overlapping_outputs_are_refused(cuda_dev):
+    import mixture_experts_routed_expert_b200 as moe
+    pool = torch.zeros(1 << 16, dtype=BF, device=cuda_dev)
+    x, y = pool[:4 * 256].view(4, 256), pool[512:512 + 4 * 256].view(4, 256)
+    w = torch.zeros(1, 256, 256, dtype=BF, device=cuda_dev)
+    off = torch.tensor([0, 4], dtype=torch.int32, device=cuda_dev)
+    inv = torch.zeros(4, 1, dtype=torch.int32, device=cuda_dev)
+    f32 = torch.zeros(2 * 256 * 256, device=cuda_dev)
+    codes, scale = torch.zeros(4, 512, dtype=torch.uint8, device=cuda_dev), torch.ones(4, 4, device=cuda_dev)
+    for bad in (lambda: moe.moe_grouped_mm(x, off, w, out=y), lambda: moe.moe_grouped_mm(x, off, w, out=x),
+                lambda: moe.moe_grouped_mm_dgrad(x, off, w, out=y),
+                lambda: moe.moe_grouped_mm_wgrad(x, x, off, out=pool[:65536].view(1, 256, 256)),
+                lambda: moe.moe_grouped_mm_wgrad(x, x, off, base=f32[:65536].view(1, 256, 256),
+                                                 out=f32[4:65540].view(1, 256, 256)),
+                lambda: moe.moe_swiglu_checkpoint(pool[:2048].view(4, 512), h=x),
+                lambda: moe.moe_swiglu_checkpoint_backward(codes, scale, x, h=x),
+                lambda: moe.moe_swiglu_checkpoint_backward(codes, scale, x, h=pool[4096:5120].view(4, 256),
+                                                           dgate_up=pool[4096:6144].view(4, 512)),
+                lambda: moe.moe_permute_rows(x, inv, out=y), lambda: moe.moe_unpermute_rows(x, inv, out=x),
+                lambda: moe.moe_unpermute_rows(pool[8192:9216].view(4, 256), inv, residual=x, out=x)):
+        with pytest.raises(ValueError, match="overlap"):
+            bad()
