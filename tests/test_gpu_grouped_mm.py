@@ -237,6 +237,36 @@ def test_several_tiles_per_cta_pair(moe, cuda_dev):
     check_sum(dx, *(t.cpu() for t in mm64(dd, off, w, True)), 1544, "input gradient")
 
 
+def test_two_row_tiles_on_a_weight_tile(moe, cuda_dev):
+    """Long reductions over more than 256 rows an expert: tiles of up to 512
+    rows, two accumulators, experts of every fill."""
+    counts = [0, 1, 16, 255, 256, 257, 272, 300, 511, 512, 513, 700, 1024, 1040] + [290] * 50
+    E, N, C, n = 64, 1192, 4104, 20157
+    assert sum(counts) == n
+    g = torch.Generator(device=cuda_dev).manual_seed(17)
+    off = offsets_of(counts, 3)
+    x = torch.randn(n + 8, C, generator=g, device=cuda_dev).to(BF)
+    x[:3], x[n + 3:] = float("nan"), float("inf")
+    w = (torch.randn(E, N, C, generator=g, device=cuda_dev) * 0.05).to(BF)
+    o = off.to(cuda_dev)
+    ws = torch.zeros(8192, dtype=torch.uint8, device=cuda_dev)
+    y = torch.full((n + 8, N), -3.0, dtype=BF, device=cuda_dev)
+    moe.moe_grouped_mm(x, o, w, out=y, workspace=ws)
+    wt = w.transpose(1, 2).contiguous()
+    dx = torch.full((n + 8, N), -3.0, dtype=BF, device=cuda_dev)
+    moe.moe_grouped_mm_dgrad(x, o, wt, out=dx, workspace=ws)
+    del wt
+    assert moe.moe_workspace_status(ws) == 0
+    for t in (y, dx):
+        assert (t[:3] == -3).all() and (t[n + 3:] == -3).all()
+    for e, a, b in spans(off, n + 8):
+        if b > a:
+            ref = x[a:b].double() @ w[e].double().t()
+            mag = x[a:b].double().abs() @ w[e].double().abs().t()
+            check_sum(y[a:b], ref.cpu(), mag.cpu(), C, "forward, expert %d" % e)
+            check_sum(dx[a:b], ref.cpu(), mag.cpu(), C, "input gradient, expert %d" % e)
+
+
 def test_same_bits_graph_and_streams(moe, cuda_dev):
     """Equal bits from repeated calls, from two streams that share a workspace,
     and from a captured graph replayed on new inputs; the status stays clean."""
