@@ -90,14 +90,14 @@ int device_of(std::initializer_list<const Tensor *> all) {
     return dev;
 }
 
-// No output may overlap an input or another output.
+// No output may overlap an input or another output (an empty one overlaps nothing).
 void apart(std::initializer_list<const Tensor *> outs, std::initializer_list<const Tensor *> ins) {
     struct Range {
         uintptr_t from, to;
     } r[16];
     size_t n = 0, n_outs = 0;
     auto add = [&](const Tensor *t) {
-        if (!t->defined()) return;
+        if (!t->defined() || t->numel() == 0) return;
         const uintptr_t p = reinterpret_cast<uintptr_t>(t->const_data_ptr());
         r[n++] = {p, p + t->nbytes()};
     };
@@ -221,7 +221,8 @@ PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tensor &given_ws = arg(a[6], "workspace");
     const int dev = device_of({&dy, &x, &off, &base, &out, &given_ws});
     // base may be out itself
-    apart({&out}, {&dy, &x, &off, &given_ws, base.defined() && out.defined() && ptr(base) == ptr(out) ? &kNone : &base});
+    const bool same = base.defined() && out.defined() && ptr(base) == ptr(out);
+    apart({&out}, {&dy, &x, &off, &given_ws, same ? &kNone : &base});
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
     if (!out.defined()) out = fresh({E, N, C}, t, dy);
     const Tensor ws = workspace_for(given_ws, dy);

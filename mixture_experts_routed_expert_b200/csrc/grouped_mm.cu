@@ -158,7 +158,10 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, const uint32_t (
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t saddr) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(saddr)
+                 : "memory");
     return v;
 }
 // True in one lane of a converged warp (the same on every call).
@@ -177,7 +180,10 @@ __device__ __forceinline__ uint32_t addr_in(uint32_t a, uint32_t rank) {
 __device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) { return addr_in(smem_u32(bar), cluster_rank() & ~1u); }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
 }
 // Arrive on the leading CTA's barrier.
@@ -405,7 +411,8 @@ __global__ void __launch_bounds__((MmCfg<OP, OUT_BF16, BN>::kThreads), 1)
             const uint64_t pol = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0;
-            uint32_t used = 0, last = 0, rused = 0, rturn = 0;   // per stage: full in use yet, its last parity; rfull likewise
+            uint32_t used = 0, last = 0;      // per stage: whether full has been armed, and its last parity
+            uint32_t rused = 0, rturn = 0;    // rfull likewise
             bool ok = true;
             for (int w = pair; w < total && ok; w += pairs) {
                 const MmTile t = mm_tile<OP, BN>(w, args, s_beg, s_end, s_tiles, MT, NT, share);

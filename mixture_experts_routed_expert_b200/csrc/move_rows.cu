@@ -43,7 +43,8 @@ __global__ void __launch_bounds__(kMaxThreads) permute_rows_kernel(
             uint4 v;
             if (FP8) {
                 float f[8];
-                restore8_e4m3(__ldg(static_cast<const uint2 *>(x) + t * V + c), __ldg(x_scale + t * (V / 16) + c / 16), f);
+                restore8_e4m3(__ldg(static_cast<const uint2 *>(x) + t * V + c),
+                              __ldg(x_scale + t * (V / 16) + c / 16), f);
                 v = pack_bf16x8(f);
             } else {
                 v = __ldg(static_cast<const uint4 *>(x) + t * V + c);

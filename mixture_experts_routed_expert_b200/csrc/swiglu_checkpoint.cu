@@ -18,8 +18,6 @@
 // time, library exponentials and quotients and a division per vector for the
 // index the forward issued 346 instructions for 8 pairs of values and took
 // 250 us.  A few rows (96 x 896): 2.4 us, the latency of one load and a launch.
-#include <float.h>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -46,7 +44,9 @@ __device__ __forceinline__ F2 f2(float lo, float hi) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
     return r;
 }
-__device__ __forceinline__ void split(F2 a, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ void split(F2 a, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
 __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
     F2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -265,14 +265,17 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel
     }
 }
 
+dim3 grid_of(int64_t blocks) {
+    return dim3((unsigned)std::min<int64_t>(blocks, (int64_t)kBlocksPerSm * num_sms()));
+}
+
 }  // namespace
 
 cudaError_t launch_swiglu_checkpoint(const void *gu, const float *weight, const int32_t *n_rows, int rows, int F,
                                      void *h, void *codes, float *scale, cudaStream_t st) {
     const int64_t blocks = ((int64_t)rows * (F / 8) + kThreads - 1) / kThreads;
-    return launch_k(swiglu_checkpoint_kernel, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)kBlocksPerSm * num_sms())),
-                    dim3(kThreads), 0, st, true, (const uint4 *)gu, weight, n_rows, rows, F, (uint4 *)h,
-                    (uint2 *)codes, scale);
+    return launch_k(swiglu_checkpoint_kernel, grid_of(blocks), dim3(kThreads), 0, st, true, (const uint4 *)gu, weight,
+                    n_rows, rows, F, (uint4 *)h, (uint2 *)codes, scale);
 }
 
 cudaError_t launch_swiglu_checkpoint_backward(const void *codes, const float *scale, const void *dh,
@@ -282,9 +285,8 @@ cudaError_t launch_swiglu_checkpoint_backward(const void *codes, const float *sc
     const int per_block = kThreads / 32 / (few ? 4 : 1);
     const int64_t blocks = ((int64_t)rows + per_block - 1) / per_block;
     auto *kernel = few ? swiglu_checkpoint_backward_kernel<4> : swiglu_checkpoint_backward_kernel<1>;
-    return launch_k(kernel, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)kBlocksPerSm * num_sms())), dim3(kThreads), 0, st, true,
-                    (const uint2 *)codes, scale, (const uint4 *)dh, weight, n_rows, rows, F, (uint4 *)dgu, (uint4 *)h,
-                    dweight);
+    return launch_k(kernel, grid_of(blocks), dim3(kThreads), 0, st, true, (const uint2 *)codes, scale,
+                    (const uint4 *)dh, weight, n_rows, rows, F, (uint4 *)dgu, (uint4 *)h, dweight);
 }
 
 }  // namespace moe

@@ -226,3 +226,32 @@ def test_overlapping_outputs_are_refused(cuda_dev):
                 lambda: moe.moe_unpermute_rows(pool[8192:9216].view(4, 256), inv, residual=x, out=x)):
         with pytest.raises(ValueError, match="overlap"):
             bad()
+
+
+@pytest.mark.parametrize("ids", ["twice", "one expert"])
+def test_an_expert_named_twice(training, cuda_dev, ids):
+    """Slots of one token on the same expert are rows of their own."""
+    T, H, F, E, K = 21, 128, 256, 4, 3
+    lay, idx = _layer(T, H, F, E, K, seed=7)
+    idx[:, 1] = idx[:, 0]
+    if ids == "one expert":
+        idx[:] = 2
+    dout = torch.randn(T, H, generator=torch.Generator().manual_seed(8)).to(BF)
+    x, gu, dn, i, w, do = (t.to(cuda_dev) for t in (lay.x, lay.gate_up, lay.down, idx, lay.w, dout))
+    out, saved = training.experts_forward(x, gu, dn, i, w)
+    ref = oracle.moe_forward_bf16(inputs.bf16_bits(lay.x), inputs.bf16_bits(lay.gate_up),
+                                  inputs.bf16_bits(lay.down), inputs.np32(idx), inputs.np32(lay.w))
+    assert_matches_oracle(out, ref, "forward")
+    got = training.experts_backward(saved, do, gu, dn)
+    for g, r, what, rounded in zip(got, _backward64(saved, lay, idx, dout, E),
+                                   ("dx", "dtop_k_weights", "dgate_up", "ddown"), (False, False, True, True)):
+        _check(g, r, what, rounded)
+
+
+def test_an_empty_output_inside_an_input(training, cuda_dev):
+    """An output without elements overlaps nothing, wherever it points."""
+    import mixture_experts_routed_expert_b200 as moe
+    pool = torch.ones(8, 128, dtype=BF, device=cuda_dev)
+    none = torch.empty(0, 1, dtype=torch.int32, device=cuda_dev)
+    out = moe.moe_unpermute_rows(pool, none, out=pool[4:4])
+    assert out.shape == (0, 128) and (pool == 1).all()
