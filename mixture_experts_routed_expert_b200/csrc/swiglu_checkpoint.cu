@@ -28,10 +28,13 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-// Blocks in the grid per SM, about eight resident: more, shorter blocks keep
-// neighbouring rows together in time (65536 x 2048 forward, 8 / 32 / 128 per
-// SM: 192 / 178 / 180 us).
-constexpr int kBlocksPerSm = 32;
+// Blocks in the grid per SM.  The forward's are those that an SM holds at once
+// (48 registers a thread): 12288 x 896 in 17.5 us, 18.8 with 32 (whose last
+// round is nearly empty), 18.4 with 8; 65536 x 2048 180 / 182 / 198 us.  The
+// backward's rows are long enough for shorter blocks, which keep neighbouring
+// rows together in time (65536 x 2048, 4 / 8 / 32 per SM: 232 / 228 / 222 us).
+constexpr int kForwardBlocks = 5;
+constexpr int kBackwardBlocks = 32;
 
 // ---- two fp32 values per instruction ---------------------------------------
 // The kernels issue as many instructions as the memory allows them time for,
@@ -136,7 +139,7 @@ __device__ __forceinline__ int64_t live_rows(const int32_t *n_rows, int rows) {
 // Half a warp per block of 128 features (gate and up), 8 values a lane; the
 // half-warps stride over the (row, block) pairs, stepping both parts of the
 // index (a 64-bit division per pair cost a quarter of the kernel).
-__global__ void __launch_bounds__(kThreads) swiglu_checkpoint_kernel(
+__global__ void __launch_bounds__(kThreads, kForwardBlocks) swiglu_checkpoint_kernel(
     const uint4 *__restrict__ gu, const float *__restrict__ weight, const int32_t *__restrict__ n_rows, int rows,
     int F, uint4 *__restrict__ h, uint2 *__restrict__ codes, float *__restrict__ scale) {
     pdl_wait();
@@ -265,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel
     }
 }
 
-dim3 grid_of(int64_t blocks) {
-    return dim3((unsigned)std::min<int64_t>(blocks, (int64_t)kBlocksPerSm * num_sms()));
+dim3 grid_of(int64_t blocks, int per_sm) {
+    return dim3((unsigned)std::min<int64_t>(blocks, (int64_t)per_sm * num_sms()));
 }
 
 }  // namespace
@@ -274,18 +277,25 @@ dim3 grid_of(int64_t blocks) {
 cudaError_t launch_swiglu_checkpoint(const void *gu, const float *weight, const int32_t *n_rows, int rows, int F,
                                      void *h, void *codes, float *scale, cudaStream_t st) {
     const int64_t blocks = ((int64_t)rows * (F / 8) + kThreads - 1) / kThreads;
-    return launch_k(swiglu_checkpoint_kernel, grid_of(blocks), dim3(kThreads), 0, st, true, (const uint4 *)gu, weight,
-                    n_rows, rows, F, (uint4 *)h, (uint2 *)codes, scale);
+    return launch_k(swiglu_checkpoint_kernel, grid_of(blocks, kForwardBlocks), dim3(kThreads), 0, st, true,
+                    (const uint4 *)gu, weight, n_rows, rows, F, (uint4 *)h, (uint2 *)codes, scale);
 }
 
 cudaError_t launch_swiglu_checkpoint_backward(const void *codes, const float *scale, const void *dh,
                                               const float *weight, const int32_t *n_rows, int rows, int F, void *dgu,
                                               void *h, float *dweight, cudaStream_t st) {
-    const bool few = rows <= 8 * num_sms();
+    // Four warps on a row while there are not rows enough to fill the GPU with one
+    // warp each, and at most a fifth of their lanes has no vector in the last of its
+    // rounds of 1024 features.  One / four warps: F=896 (an eighth idle) 2000 rows
+    // 7.9 / 6.7 us, 6000 rows 15.8 / 14.7 us, 12288 rows 25.3 / 26.0 us; F=2048, 6000
+    // rows 26.9 / 24.8 us; F=768 (a quarter), 3000 rows 7.6 / 8.3 us; F=1152, 6000 rows
+    // 17.3 / 20.9 us.
+    const int rounds = (F + 1023) / 1024;
+    const bool few = rows <= 8 * num_sms() || (rows <= 48 * num_sms() && rounds * 1024 <= F + F / 4);
     const int per_block = kThreads / 32 / (few ? 4 : 1);
     const int64_t blocks = ((int64_t)rows + per_block - 1) / per_block;
     auto *kernel = few ? swiglu_checkpoint_backward_kernel<4> : swiglu_checkpoint_backward_kernel<1>;
-    return launch_k(kernel, grid_of(blocks), dim3(kThreads), 0, st, true, (const uint2 *)codes, scale,
+    return launch_k(kernel, grid_of(blocks, kBackwardBlocks), dim3(kThreads), 0, st, true, (const uint2 *)codes, scale,
                     (const uint4 *)dh, weight, n_rows, rows, F, (uint4 *)dgu, (uint4 *)h, dweight);
 }
 

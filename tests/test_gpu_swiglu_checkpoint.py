@@ -193,3 +193,10 @@ def test_offsets_past_32_bits(moe, cuda_dev):
     _, rh, _ = swiglu_backward64(restore64(codes[-last:].cpu(), scale[-last:].cpu()), d)
     _near(hb[-last:], rh, (BF16_HALF + ARITH) * rh.abs(), "h")
     assert (dgu[:1000] == 0).all() and (dp[:-last] == 0).all() and (dgu[-last:] != 0).float().mean() > 0.9
+
+
+@pytest.mark.parametrize("rows,F", [(1300, 384), (1300, 896), (2100, 1152), (7300, 896)])
+def test_rows_beyond_one_round(moe, cuda_dev, rows, F):
+    """One and four warps a row, several rows a block: the same formulas."""
+    test_forward(moe, cuda_dev, rows, F, True)
+    test_backward(moe, cuda_dev, rows, F, True)
