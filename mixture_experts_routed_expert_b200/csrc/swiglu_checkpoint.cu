@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks) swiglu_checkpoint_ke
     }
 }
 
-// WPR warps per row: one for many rows, four for few (the row's loads then
-// all go out at once).
-template <int WPR>
+// LPR lanes per row: a warp's for many rows, four warps' for few (the row's
+// loads then all go out at once), half a warp's for short ones.
+template <int LPR>
 __global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel(
     const uint2 *__restrict__ codes, const float *__restrict__ scale, const uint4 *__restrict__ dh,
     const float *__restrict__ weight, const int32_t *__restrict__ n_rows, int rows, int F, uint4 *__restrict__ dgu,
@@ -200,10 +200,11 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel
     pdl_wait();
     pdl_launch_dependents();
     const int NB = F / 128, V = F / 8, lane = lane_id(), warp = threadIdx.x >> 5;
+    constexpr int kRows = kThreads / LPR;      // of a block at a time
     const int64_t live = live_rows(n_rows, rows);
-    const int64_t stride = (int64_t)gridDim.x * (kThreads / 32 / WPR);
-    for (int64_t r0 = (int64_t)blockIdx.x * (kThreads / 32 / WPR); r0 < live; r0 += stride) {
-        const int64_t r = r0 + warp / WPR;
+    const int64_t stride = (int64_t)gridDim.x * kRows;
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < live; r0 += stride) {
+        const int64_t r = r0 + threadIdx.x / LPR;
         float dot = 0.f;
         if (r < live) {
             const float p = weight ? __ldg(weight + r) : 1.0f;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel
             const uint4 *dr = dh + r * V;
             uint4 *gr = dgu + r * 2 * V, *hr = h ? h + r * V : nullptr;
             F2 dot2 = f2(0.f, 0.f);
-            int c = (warp % WPR) * 32 + lane;
+            int c = threadIdx.x % LPR;
             uint2 qg = make_uint2(0, 0), qu = qg;
             uint4 vd = make_uint4(0, 0, 0, 0);
             float sg = 0.f, su = 0.f;
@@ -225,12 +226,12 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel
                 vd = __ldg(dr + at);
             };
             load(c);
-            for (; c < V; c += 32 * WPR) {
+            for (; c < V; c += LPR) {
                 F2 g[4], u[4];
                 restore8(qg, sg, g);
                 restore8(qu, su, u);
                 const F2 d[4] = {unpack2(vd.x), unpack2(vd.y), unpack2(vd.z), unpack2(vd.w)};
-                load(c + 32 * WPR);
+                load(c + LPR);
                 uint32_t dg[4], du[4], o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -251,15 +252,15 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_checkpoint_backward_kernel
         }
         if (dweight) {
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-            if (WPR == 1) {
-                if (lane == 0 && r < live) dweight[r] = dot;
+            for (int o = LPR < 32 ? LPR / 2 : 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+            if (LPR <= 32) {
+                if (threadIdx.x % LPR == 0 && r < live) dweight[r] = dot;
             } else {
                 if (lane == 0) s_dot[warp] = dot;
                 __syncthreads();
-                if (lane == 0 && warp % WPR == 0 && r < live) {
+                if (threadIdx.x % LPR == 0 && r < live) {
                     float sum = s_dot[warp];
-                    for (int i = 1; i < WPR; ++i) sum += s_dot[warp + i];
+                    for (int i = 1; i < LPR / 32; ++i) sum += s_dot[warp + i];
                     dweight[r] = sum;
                 }
                 __syncthreads();
@@ -292,9 +293,15 @@ cudaError_t launch_swiglu_checkpoint_backward(const void *codes, const float *sc
     // 17.3 / 20.9 us.
     const int rounds = (F + 1023) / 1024;
     const bool few = rows <= 8 * num_sms() || (rows <= 48 * num_sms() && rounds * 1024 <= F + F / 4);
-    const int per_block = kThreads / 32 / (few ? 4 : 1);
+    // Half a warp on a short row, of 16, 32 or 48 vectors: more rows at once, and no idle
+    // halves (65536 rows, a warp / half: F=128 28.2 / 17.9 us, 256 34.3 / 32.0 us, 384
+    // 58.5 / 46.4 us; 512 64 / 63 us, 768 90.2 / 93.2 us)
+    const bool half = !few && F <= 384;
+    const int per_block = kThreads / (few ? 128 : half ? 16 : 32);
     const int64_t blocks = ((int64_t)rows + per_block - 1) / per_block;
-    auto *kernel = few ? swiglu_checkpoint_backward_kernel<4> : swiglu_checkpoint_backward_kernel<1>;
+    auto *kernel = few    ? swiglu_checkpoint_backward_kernel<128>
+                   : half ? swiglu_checkpoint_backward_kernel<16>
+                          : swiglu_checkpoint_backward_kernel<32>;
     return launch_k(kernel, grid_of(blocks, kBackwardBlocks), dim3(kThreads), 0, st, true, (const uint2 *)codes, scale,
                     (const uint4 *)dh, weight, n_rows, rows, F, (uint4 *)dgu, (uint4 *)h, dweight);
 }

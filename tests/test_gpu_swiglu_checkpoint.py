@@ -195,8 +195,8 @@ def test_offsets_past_32_bits(moe, cuda_dev):
     assert (dgu[:1000] == 0).all() and (dp[:-last] == 0).all() and (dgu[-last:] != 0).float().mean() > 0.9
 
 
-@pytest.mark.parametrize("rows,F", [(1300, 384), (1300, 896), (2100, 1152), (7300, 896)])
+@pytest.mark.parametrize("rows,F", [(1300, 128), (1301, 256), (1300, 384), (1300, 896), (2100, 1152), (7300, 896)])
 def test_rows_beyond_one_round(moe, cuda_dev, rows, F):
-    """One and four warps a row, several rows a block: the same formulas."""
+    """Half a warp, one and four on a row, several rows a block: the same formulas."""
     test_forward(moe, cuda_dev, rows, F, True)
     test_backward(moe, cuda_dev, rows, F, True)
