@@ -8,8 +8,8 @@
 // unpermute reads its K rows and writes one.
 //
 // What bounds them: memory.  8192 tokens x 8 slots x 7168 columns: permute from
-// codes 171 us for 1.0 GB, unpermute 182 us for 1.2 GB (5.8 and 6.5 TB/s); 2047
-// tokens 46 us.  2048 tokens x 6 x 1280 (42 MB): unpermute 9.9 us, of which 6.4
+// codes 168 us for 1.0 GB, unpermute 173 us for 1.2 GB (5.9 and 6.8 TB/s); 2047
+// tokens 42 us.  2048 tokens x 6 x 1280 (42 MB): unpermute 9.9 us, of which 6.4
 // are the bytes.
 #include "common.cuh"
 #include "internal.h"
@@ -23,8 +23,8 @@ namespace {
 constexpr int kMaxThreads = 256;
 constexpr int kBatch = 4;      // slots of a token whose loads go out together
 
-// A block holds blockDim.y tokens, blockDim.x threads each; a thread takes 8
-// columns at a time.
+// A block holds blockDim.y tokens of a stretch of columns, blockDim.x threads
+// each; a thread takes 8 columns.
 template <bool FP8>
 __global__ void __launch_bounds__(kMaxThreads) permute_rows_kernel(
     const void *__restrict__ x, const float *__restrict__ x_scale, const int32_t *__restrict__ inv,
@@ -32,14 +32,15 @@ __global__ void __launch_bounds__(kMaxThreads) permute_rows_kernel(
     float *__restrict__ row_weights) {
     pdl_wait();
     pdl_launch_dependents();
-    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.x * blockDim.y) {
+    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+    for (int64_t t = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.y * blockDim.y) {
         const int32_t *pos = inv + t * K;
-        if (row_weights)
+        if (row_weights && blockIdx.x == 0)
             for (int k = threadIdx.x; k < K; k += blockDim.x) {
                 const int p = __ldg(pos + k);
                 if (p >= 0 && p < n_out) row_weights[p] = __ldg(weights + t * K + k);
             }
-        for (int c = threadIdx.x; c < V; c += blockDim.x) {
+        if (c < V) {
             uint4 v;
             if (FP8) {
                 float f[8];
@@ -67,14 +68,15 @@ __global__ void __launch_bounds__(kMaxThreads, 6) unpermute_rows_kernel(
     float *__restrict__ dweights) {
     pdl_wait();
     pdl_launch_dependents();
-    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.x * blockDim.y) {
+    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+    for (int64_t t = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.y * blockDim.y) {
         const int32_t *pos = inv + t * K;
-        if (dweights)
+        if (dweights && blockIdx.x == 0)
             for (int k = threadIdx.x; k < K; k += blockDim.x) {
                 const int p = __ldg(pos + k);
                 dweights[t * K + k] = p >= 0 && p < n_in ? __ldg(drow + p) : 0.0f;
             }
-        for (int c = threadIdx.x; c < V; c += blockDim.x) {
+        if (c < V) {
             const uint4 vr = residual ? __ldg(residual + t * V + c) : make_uint4(0, 0, 0, 0);
             float acc[8] = {};
             for (int k0 = 0; k0 < K; k0 += kBatch) {
@@ -113,33 +115,41 @@ __global__ void __launch_bounds__(kMaxThreads, 6) unpermute_rows_kernel(
     }
 }
 
-// Threads of a token: the fewest warps that go over its V vectors in
-// ceil(V / 256) rounds; a block holds as many tokens as fit in 256 threads.
-dim3 block_of(int V) {
-    const int rounds = (V + kMaxThreads - 1) / kMaxThreads;
+// A token's V vectors in the fewest equal stretches of at most 128 threads (whole
+// warps), a block for each: 7168 columns, a block on a whole token / on a stretch:
+// 1 token 6.3 / 3.0 us, 128 tokens 12.3 / 5.4 us, 2047 tokens (permute) 46.1 / 42.2
+// us.  Stretches of 256 threads are the same to 4 % slower (permute, 1280 columns).
+// A block holds as many tokens as fit in 256 threads.
+struct Shape {
+    dim3 grid, block;
+};
+Shape shape_of(int64_t T, int V) {
+    const int rounds = (V + kMaxThreads / 2 - 1) / (kMaxThreads / 2);
     const int tx = ((V + rounds - 1) / rounds + 31) / 32 * 32;
-    return dim3(tx, std::max(1, kMaxThreads / tx));
-}
-dim3 grid_of(int64_t T, dim3 block) {
-    return dim3((unsigned)std::min<int64_t>((T + block.y - 1) / block.y, 64LL * num_sms()));
+    const int pieces = (V + tx - 1) / tx;
+    Shape s;
+    s.block = dim3(tx, kMaxThreads / tx);
+    const int64_t groups = (T + s.block.y - 1) / s.block.y;
+    s.grid = dim3(pieces, (unsigned)std::min<int64_t>(groups, std::max(1, 64 * num_sms() / pieces)));
+    return s;
 }
 
 }  // namespace
 
 cudaError_t launch_permute_rows(const void *x, const float *x_scale, const int32_t *inv, const float *weights,
                                 int64_t T, int K, int H, int n_out, void *out, float *row_weights, cudaStream_t st) {
-    const dim3 b = block_of(H / 8);
+    const Shape s = shape_of(T, H / 8);
     auto *kernel = x_scale ? permute_rows_kernel<true> : permute_rows_kernel<false>;
-    return launch_k(kernel, grid_of(T, b), b, 0, st, true, x, x_scale, inv, weights, (int)T, K, H / 8,
+    return launch_k(kernel, s.grid, s.block, 0, st, true, x, x_scale, inv, weights, (int)T, K, H / 8,
                     n_out, (uint4 *)out, row_weights);
 }
 
 cudaError_t launch_unpermute_rows(const void *y, bool y_fp32, const int32_t *inv, const void *residual,
                                   const float *drow, int64_t T, int K, int H, int n_in, void *out, float *dweights,
                                   cudaStream_t st) {
-    const dim3 b = block_of(H / 8);
+    const Shape s = shape_of(T, H / 8);
     auto *kernel = y_fp32 ? unpermute_rows_kernel<true> : unpermute_rows_kernel<false>;
-    return launch_k(kernel, grid_of(T, b), b, 0, st, true, y, inv, (const uint4 *)residual, drow, (int)T, K,
+    return launch_k(kernel, s.grid, s.block, 0, st, true, y, inv, (const uint4 *)residual, drow, (int)T, K,
                     H / 8, n_in, (uint4 *)out, dweights);
 }
 
