@@ -66,6 +66,10 @@ constexpr int kABytes = kBM * 128;
 constexpr int kOutStage = 8 * 32 * 64;         // per epilogue warp 32 rows x 32 columns of bf16
 constexpr int kChunkBytes = 64 * 128;          // MN-major: 64 elements x 64 reduction rows
 constexpr int kBand = 8;                       // row tiles of a band
+// Rows per TMA box of a K-major B: few, so that little is read behind a short
+// tile's rows.  70 experts of 19 rows, N=3352 C=536, boxes of 128 / 64 / 32 rows:
+// 78 / 65 / 59 us; full tiles alike.
+constexpr int kBoxRows = 32;
 // k-blocks that the tensor cores sum for an fp32 output before the epilogue
 // takes the partial sum into its registers.  Their accumulation truncates: a
 // sum of K products came out 9.5e-10 K too small, relatively (K = 512: 4.8e-7,
@@ -89,6 +93,7 @@ struct MmCfg {
     static constexpr int kEpiWarps = OP == kWgrad && !OUT_BF16 ? 16 : 8;
     static constexpr int kSets = kEpiWarps / 4;
     static constexpr int kThreads = 64 + 32 * kEpiWarps + (OP == kWgrad ? 32 : 0);
+    static_assert(BN / 2 % kBoxRows == 0, "the boxes of a stage lie within its B region");
     static_assert(kRaggedDelay + 2 <= kStages && (OP != kWgrad || BN / 2 % 64 == 0), "");
     static size_t smem_bytes(int E) { return 1024 + kRingBytes + 1024 + kOutStage + align_up(12 * (size_t)(E + 1), 16); }
 };
@@ -98,7 +103,6 @@ struct MmArgs {
     int rows;                 // rows of the row matrices
     int E, M, N;              // experts; A-side extent; B-side extent (weight gradient)
     int red;                  // reduction extent (forward, input gradient)
-    int box_rows;             // rows per TMA box of a K-major B
     void *out;
     const float *base;        // weight gradient: added to the product (may be out itself), or null
     int split;                // pairs of a cluster that share a tile
@@ -420,8 +424,8 @@ __global__ void __launch_bounds__((MmCfg<OP, OUT_BF16, BN>::kThreads), 1)
                 const int KB = (t.red + kBK - 1) / kBK;
                 const int half = ((t.nrows + 15) & ~15) / 2;         // B rows of each CTA
                 const int m0 = t.m0 + rank * kBM, row0 = t.row0 + rank * half;
-                const int nbox = OP == kWgrad ? (half + 63) / 64 : (half + args.box_rows - 1) / args.box_rows;
-                const int box_bytes = OP == kWgrad ? kChunkBytes : args.box_rows * 128;
+                const int nbox = OP == kWgrad ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
+                const int box_bytes = OP == kWgrad ? kChunkBytes : kBoxRows * 128;
                 const uint32_t bytes = kABytes + nbox * box_bytes;
                 const bool ends_ragged = ragged_end<OP>(t);
                 for (int i = 0; i < KB; ++i) {
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__((MmCfg<OP, OUT_BF16, BN>::kThreads), 1)
                         if (OP == kWgrad)
                             tma_load_2d_pair(sB + b * kChunkBytes, &tmB, bar, row0 + 64 * b, k0, pol);
                         else
-                            tma_load_2d_pair(sB + b * box_bytes, &tmB, bar, k0, row0 + b * args.box_rows, pol);
+                            tma_load_2d_pair(sB + b * box_bytes, &tmB, bar, k0, row0 + b * kBoxRows, pol);
                     }
                     if (++stage == C::kStages) { stage = 0; phase ^= 1; }
                 }
@@ -925,12 +929,11 @@ cudaError_t launch_grouped_mm(const void *x, const void *w, const int32_t *offse
     // 1024 rows 52.2 / 53.1 us; at 2048 rows even experts 55.1 / 56.6 us, but
     // Zipf(1.1) experts 51.2 / 49.2 us, and 66.8 / 56.7 us at 4096.
     const bool few = rows <= (int64_t)16 * E;
-    a.box_rows = few ? 32 : 128;   // at most BN / 2: the boxes of a stage lie within its B region
     a.out = out;
     a.status = status;
     CUtensorMap ta, tb;
     if (!make_tmap_3d(&ta, w, E, N, C, transpose ? kBK : kBM) ||
-        !make_tmap(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, rows, red, a.box_rows))
+        !make_tmap(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, rows, red, kBoxRows))
         return cudaErrorInvalidValue;
     const ZeroMaps z = {};   // not used by these two
     // at most one partly filled row tile for each expert that can have rows
