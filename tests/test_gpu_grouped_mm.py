@@ -386,3 +386,40 @@ def test_another_stream_keeps_its_tensors(moe, cuda_dev):
         torch.full((512, 512), float("nan"), dtype=BF, device=cuda_dev)      # takes freed memory at once
     torch.cuda.synchronize()
     assert all(torch.equal(t, want) for t in outs)
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_outputs_of_an_odd_number_of_16_byte_units(moe, cuda_dev, few):
+    """bf16 rows that begin in the middle of a 32-byte sector, many tiles an SM
+    pair, edges of every kind: exact to the formulas, and nothing around the
+    outputs is touched."""
+    E, N, C = 41, 776, 424
+    g = torch.Generator().manual_seed(12)
+    counts = torch.randint(0, 9 if few else 70, (E,), generator=g).tolist()
+    counts[3], counts[7] = 0, 1 if few else 300
+    off, x, dy, w = _inputs(counts, N, C, slack=5, seed=13)
+    o, xd, dd, wd = (t.to(cuda_dev) for t in (off, x, dy, w))
+    rows, live = x.shape[0], int(off[-1])
+    ws = torch.zeros(8192, dtype=torch.uint8, device=cuda_dev)
+
+    def guarded(*shape):
+        n = 1
+        for d in shape:
+            n *= d
+        buf = torch.full((n + 128,), 7.0, dtype=BF, device=cuda_dev)
+        return buf, buf[64:64 + n].view(*shape)
+
+    by, y = guarded(rows, N)
+    bx, dx = guarded(rows, C)
+    bw, dw = guarded(E, N, C)
+    for _ in range(2):
+        moe.moe_grouped_mm(xd, o, wd, out=y, workspace=ws)
+        moe.moe_grouped_mm_dgrad(dd, o, wd, out=dx, workspace=ws)
+        moe.moe_grouped_mm_wgrad(dd, xd, o, out=dw, workspace=ws)
+    assert moe.moe_workspace_status(ws) == 0
+    for b in (by, bx, bw):
+        assert (b[:64] == 7).all() and (b[-64:] == 7).all()
+    assert (y[live:] == 7).all() and (dx[live:] == 7).all()
+    for got, (ref, mag), terms in ((y, mm64(x, off, w, False), C), (dx, mm64(dy, off, w, True), N)):
+        check_sum(got[:live], ref[:live], mag[:live], terms, "product")
+    check_sum(dw, *wgrad64(dy, x, off), max(counts), "weight gradient")
